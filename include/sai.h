@@ -22,6 +22,13 @@
  * sai_distill_target_window_range, sai_count_valid_rows and
  * sai_distill_kl_ex (a batch-wide N).
  *
+ * Before and after the loss, the indexer in 8 bits: sai_q8_cache_write /
+ * sai_q8_cache_read (rows quantised as they are written into a paged cache,
+ * and read back), sai_indexer_scores (the scores sai_indexer_topk selects
+ * from, for whole sequences and for single tokens) and
+ * sai_indexer_scores_backward (dscores to the indexer's queries, keys and head
+ * weights, from the 8-bit codes the forward kept).
+ *
  * Conventions for every call
  *   - Tensor arguments are DEVICE pointers to dense row-major (C-contiguous)
  *     arrays, owned by the caller. The library never allocates device memory
@@ -498,6 +505,150 @@ sai_status sai_distill_kl_noalloc(const float *p, const float *scores, const uin
  */
 sai_status sai_indexer_topk(const float *index_scores, const int32_t *doc_start, int B, int S, int cr, int K,
                             int32_t *idx, float *sel_scores, uint8_t *valid, void *stream);
+
+/* Element types of the 16- and 32-bit rows, and formats of the 8-bit codes. */
+enum { SAI_TYPE_BF16 = 0, SAI_TYPE_FP16 = 1, SAI_TYPE_FP32 = 2 };
+enum { SAI_CODE_INT8 = 0, SAI_CODE_E4M3 = 1 };
+
+/*
+ * sai_q8_cache_write -- rows quantised to 8 bits as they are written into a
+ * cache of pages.
+ *
+ * The source pages name 8-bit formats for the indexer's products (page "Docker
+ * Build for DeepSeek-v4": FP8 and FP4 indexer recipes) without their
+ * arithmetic, which is this library's own. `group` consecutive values of a row
+ * share a scale; with amax their largest magnitude
+ *
+ *   SAI_CODE_INT8:  code = rint(127 x / amax),   scale = amax / 127
+ *   SAI_CODE_E4M3:  code = e4m3(448 x / amax),   scale = amax / 448
+ *
+ * rounded to the nearest code, ties to even (the code of the exact quotient),
+ * the scale in fp32; amax = 0 gives codes 0 and scale 0, a NaN or infinity in
+ * the group gives codes 0 and scale NaN. The value a code stands for is
+ * code * scale.
+ *
+ * Entry pos of sequence b is row pos % page of page block_table[b][pos / page].
+ * Row i < n_new[b] of sequence b is written to entry start[b] + i; rows from
+ * n_new[b] on are not read (a padded batch), and no other part of the cache is
+ * written.
+ *
+ *   x           rows of type x_type: element e of row (b, i) is
+ *               x[b*stride_b + i*stride_n + e] (strides in elements, >= 0;
+ *               aligned to the element; rows on 16-byte boundaries load
+ *               fastest)
+ *   start       [B] int32 or NULL (0); n_new [B] int32 or NULL (n)
+ *   block_table [B,max_pages] int32, or NULL: sequence b owns page b
+ *               (max_pages = 1, n_pages >= B)
+ *   cache       [n_pages,page,D] 8-bit codes, 16-byte aligned
+ *   scales      [n_pages,page,D/group] fp32
+ *   d_err       optional device int32: SAI_ERR_INDEX if a row's entry lies
+ *               outside the table or its page id outside [0, n_pages); such
+ *               a row is not written
+ *
+ * Rows of one call must go to different entries (two sequences that share a
+ * page must not both write to it): of two rows for one entry, codes and scale
+ * may come from different ones. Sizes: group one of 32, 64, 128, 256, 512,
+ * D % group == 0, max_pages*page < 2^31. Errors: SAI_ERR_NULL, SAI_ERR_SHAPE,
+ * SAI_ERR_ALIGN, SAI_ERR_UNSUPPORTED (group, type or code), SAI_ERR_CUDA.
+ */
+sai_status sai_q8_cache_write(const void *x, int x_type, int64_t stride_b, int64_t stride_n, const int32_t *start,
+                              const int32_t *n_new, const int32_t *block_table, int B, int n, int D, int group,
+                              int code, int n_pages, int page, int max_pages, void *cache, float *scales,
+                              int32_t *d_err, void *stream);
+
+/*
+ * sai_q8_cache_read -- entries of the cache as 16- or 32-bit rows.
+ *
+ *   out[b,i,:] = code * scale of entry pos, rounded once to out_type
+ *   pos = idx[b,i], or (idx NULL) start[b] + i
+ *
+ * A row of zeros is written where idx is -1 and where pos >= lens[b] (entries
+ * behind the sequence's end). An entry outside the table's capacity, a page id
+ * outside [0, n_pages) or an idx below -1 gives a row of zeros and
+ * SAI_ERR_INDEX in *d_err.
+ *
+ *   idx   [B,n] int32 or NULL (e.g. the selection of sai_indexer_topk);
+ *         start [B] int32 or NULL, only without idx; lens [B] int32 or NULL
+ *   out   [B,n,D] of out_type, 16-byte aligned
+ *
+ * The rest as for sai_q8_cache_write.
+ */
+sai_status sai_q8_cache_read(const void *cache, const float *scales, const int32_t *idx, const int32_t *start,
+                             const int32_t *lens, const int32_t *block_table, int B, int n, int D, int group,
+                             int code, int n_pages, int page, int max_pages, void *out, int out_type,
+                             int32_t *d_err, void *stream);
+
+/*
+ * sai_indexer_scores -- the lightning indexer's scores from 8-bit queries and
+ * 8-bit cached keys.
+ *
+ *   s[b,t,j] = k_scale[b,j] * sum_h w[b,t,h] q_scale[b,t,h] relu(<q8[b,t,h,:], k8[b,j,:]>)
+ *
+ * for the candidates j of token t, and -inf elsewhere. With pos = q_start[b] +
+ * t and d0 = clamp(doc_start[b,t], 0, pos), block j is a candidate iff
+ * (j+1)*cr - 1 <= pos, j*cr >= d0 and j < k_len[b] (the rule of
+ * sai_indexer_topk, which takes these scores). The products of the codes are
+ * added exactly, the heads in fp32. Scales must not be negative (those of
+ * sai_q8_cache_write are not).
+ *
+ *   q8       [B,S,H,D] int8, 16-byte aligned; q_scale, w [B,S,H] fp32
+ *   cache    [n_pages,page,D] int8, 16-byte aligned; k_scale [n_pages,page]
+ *            fp32 (group = D); block_table as for sai_q8_cache_write
+ *   q_start  [B] int32 or NULL (0): position of a sequence's first query;
+ *   k_len    [B] int32 or NULL (P): entries its cache holds;
+ *   doc_start [B,S] int32 or NULL
+ *   scores   [B,S,P] fp32, written
+ *   d_err    optional: SAI_ERR_INDEX if a candidate's page id lies outside
+ *            [0, n_pages) (its scores are -inf), SAI_ERR_TIMEOUT if a wait
+ *            inside the kernel gave up
+ *
+ * S = 1 with a block table is the decoding form. Sizes: 1 <= H <= 128, D one
+ * of 32, 64, 128, P <= max_pages*page; with more than one page a sequence,
+ * page a multiple of 128 or one of 8, 16, 32, 64. Errors: SAI_ERR_NULL,
+ * SAI_ERR_SHAPE, SAI_ERR_ALIGN, SAI_ERR_UNSUPPORTED, SAI_ERR_CUDA.
+ */
+sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const float *w, const int8_t *cache,
+                              const float *k_scale, const int32_t *block_table, const int32_t *q_start,
+                              const int32_t *k_len, const int32_t *doc_start, int B, int S, int H, int D, int P,
+                              int n_pages, int page, int max_pages, int cr, float *scores, int32_t *d_err,
+                              void *stream);
+
+/*
+ * sai_indexer_scores_backward -- gradient of sai_indexer_scores from the 8-bit
+ * codes that the forward kept.
+ *
+ * With G[t,j] the sum of dscores[t,k] over the slots k with idx[t,k] = j (idx
+ * NULL, the dense warm-up stage: G = dscores) where j is a candidate of t, 0
+ * elsewhere, and m[t,h,j] = 1 where <q8[t,h], k8[j]> > 0:
+ *
+ *   dq[t,h,:] = w[t,h] * sum_j m G[t,j] k_scale[j] k8[j,:]
+ *   dk[j,:]   = sum_{t,h} m G[t,j] w[t,h] q_scale[t,h] q8[t,h,:]
+ *   dw[t,h]   = q_scale[t,h] * sum_j G[t,j] k_scale[j] relu(<q8[t,h], k8[j]>)
+ *
+ * the gradients with respect to the values that the codes stand for (rounding
+ * to codes passes a gradient on as it is). An entry with G = 0 contributes
+ * nothing, whatever its scale holds. Deterministic: the same inputs give the
+ * same bits.
+ *
+ *   dscores  [B,S,K] fp32 (sai_distill_kl's); idx [B,S,K] int32, or NULL
+ *            (K = P); an entry outside {-1} U [0,P) is ignored and sets
+ *            SAI_ERR_INDEX in *d_err
+ *   q8       [B,S,H,D] int8; q_scale, w [B,S,H] fp32
+ *   k8       [B,P,D] int8, k_scale [B,P] fp32 (a cache of one page a sequence)
+ *   t_begin  sequence position of token 0 (0: whole sequences)
+ *   dq       [B,S,H,D] bf16, dk [B,P,D] bf16, dw [B,S,H] fp32, written
+ *   workspace device scratch of sai_indexer_scores_backward_workspace_bytes()
+ *            bytes, 16-byte aligned; its content need not be kept
+ *
+ * dk of tokens split over calls (t_begin) is the sum of the calls' dk. Errors:
+ * as for sai_indexer_scores, and SAI_ERR_WORKSPACE.
+ */
+size_t sai_indexer_scores_backward_workspace_bytes(int B, int S, int H, int D, int P);
+sai_status sai_indexer_scores_backward(const float *dscores, const int32_t *idx, const int8_t *q8,
+                                       const float *q_scale, const float *w, const int8_t *k8, const float *k_scale,
+                                       const int32_t *doc_start, int B, int S, int H, int D, int P, int K, int cr,
+                                       int t_begin, uint16_t *dq, uint16_t *dk, float *dw, void *workspace,
+                                       size_t ws_bytes, int32_t *d_err, void *stream);
 
 #ifdef __cplusplus
 }

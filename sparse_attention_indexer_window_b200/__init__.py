@@ -9,6 +9,15 @@ fallback here: if ``libsai.so`` is missing the import fails.
     distill_kl(p, scores, valid, coeff, want_grad=True, workspace=None, n_rows=None) -> (loss[1], dscores)
     distill_target_window(Q, Kw, pool, idx, W, cr, scale, ...) -> [B,S,K] fp32 (window band inside, Q read once)
 
+The indexer in 8 bits, before and after the loss:
+
+    q8_quantize(x)                                             -> (codes, scales)
+    q8_cache_write(x, cache, scales, start=, n_new=, block_table=)   rows quantised into a paged cache
+    q8_cache_read(cache, scales, idx=, lens=, block_table=)    -> [B,n,D] bf16/fp16/fp32
+    indexer_scores(q8, q_scale, w, cache, k_scale, cr, ...)    -> [B,S,P] fp32, indexer_topk's input
+    indexer_scores_backward(dscores, idx, q8, q_scale, w, k8, k_scale, cr) -> (dq, dk, dw)
+    indexer_distill_step(...)                                  -> (loss, dq, dk, dw), the whole path
+
 The token-range calls (window_lse_range, distill_target_range,
 count_valid_rows) serve a batch split across GPUs by sequence position; see
 shard.py for the call sequence.
@@ -92,6 +101,18 @@ _lib.sai_status_string.argtypes = [_I]
 _lib.sai_status_string.restype = ctypes.c_char_p
 _lib.sai_indexer_topk.argtypes = [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P]
 _lib.sai_indexer_topk.restype = _I
+_I64 = ctypes.c_int64
+_lib.sai_q8_cache_write.argtypes = [_P, _I, _I64, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]
+_lib.sai_q8_cache_write.restype = _I
+_lib.sai_q8_cache_read.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P]
+_lib.sai_q8_cache_read.restype = _I
+_lib.sai_indexer_scores.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]
+_lib.sai_indexer_scores.restype = _I
+_lib.sai_indexer_scores_backward_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+_lib.sai_indexer_scores_backward_workspace_bytes.restype = ctypes.c_size_t
+_lib.sai_indexer_scores_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P,
+                                             _P, _P, ctypes.c_size_t, _P, _P]
+_lib.sai_indexer_scores_backward.restype = _I
 _lib.sai_version.argtypes = []
 _lib.sai_version.restype = _I
 
@@ -502,3 +523,268 @@ def indexer_topk(index_scores: torch.Tensor, cr: int, K: int, doc_start: Optiona
                _ptr(idx), _ptr(sel_scores), _ptr(valid))
     _check(st, "sai_indexer_topk")
     return idx, sel_scores, valid
+
+
+# ------------------------------------------------------- the indexer in 8 bits
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _on(dev: torch.device, **tensors):
+    """Every given tensor lives on dev."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _row_type(dtype, name: str) -> int:
+    if dtype not in _ROW_TYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
+    return _ROW_TYPES[dtype]
+
+
+def _cache_args(cache: torch.Tensor, scales: torch.Tensor, block_table: Optional[torch.Tensor], B: int):
+    """(code, n_pages, page, D, group, max_pages) of a checked cache."""
+    if cache.dtype not in _CODES:
+        raise TypeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
+    if cache.dim() != 3:
+        raise ValueError(f"cache must be [n_pages,page,D], got {tuple(cache.shape)}")
+    n_pages, page, D = cache.shape
+    _want(cache, "cache", cache.dtype)
+    if scales.dim() != 3 or tuple(scales.shape[:2]) != (n_pages, page) or D == 0 or scales.shape[2] == 0 \
+            or D % scales.shape[2]:
+        raise ValueError(f"scales must be [n_pages,page,D/group] beside a cache of {tuple(cache.shape)}, "
+                         f"got {tuple(scales.shape)}")
+    _want(scales, "scales", torch.float32)
+    if block_table is None:
+        max_pages = 1
+    else:
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [B,max_pages] with B = {B}, got {tuple(block_table.shape)}")
+        _want(block_table, "block_table", torch.int32)
+        max_pages = block_table.shape[1]
+    return _CODES[cache.dtype], n_pages, page, D, D // scales.shape[2], max_pages
+
+
+def q8_cache_write(x: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
+                   start: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+                   block_table: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None) -> None:
+    """Rows x [B,n,D] (bf16, fp16 or fp32; any strides over B and n) quantised
+    into the entries start[b] .. start[b]+n_new[b]-1 of each sequence, through
+    sai_q8_cache_write. cache [n_pages,page,D] is int8 or float8_e4m3fn,
+    scales [n_pages,page,D/group] fp32; block_table [B,max_pages] int32 names
+    each sequence's pages (None: sequence b owns page b). Rows of one call
+    must go to different entries."""
+    t = _row_type(x.dtype, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B,n,D], got {tuple(x.shape)}")
+    B, n, D = x.shape
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if D > 1 and x.stride(2) != 1:
+        raise ValueError("the values of a row of x must be contiguous")
+    code, n_pages, page, Dc, group, max_pages = _cache_args(cache, scales, block_table, B)
+    if Dc != D:
+        raise ValueError(f"x has rows of {D} values, the cache of {Dc}")
+    _want(start, "start", torch.int32, (B,))
+    _want(n_new, "n_new", torch.int32, (B,))
+    _want(err, "err", torch.int32)
+    _on(x.device, cache=cache, scales=scales, start=start, n_new=n_new, block_table=block_table, err=err)
+    st = _call(_lib.sai_q8_cache_write, x.device, _ptr(x), t, x.stride(0), x.stride(1), _ptr(start), _ptr(n_new),
+               _ptr(block_table), B, n, D, group, code, n_pages, page, max_pages, _ptr(cache), _ptr(scales), _ptr(err))
+    _check(st, "sai_q8_cache_write")
+
+
+def q8_cache_read(cache: torch.Tensor, scales: torch.Tensor, idx: Optional[torch.Tensor] = None,
+                  n: Optional[int] = None, start: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                  block_table: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Entries of the cache as rows [B,n,D] of dtype, through
+    sai_q8_cache_read: the entries idx [B,n] names (-1: a row of zeros), or
+    without idx the n entries from start[b] (None: 0) on. Entries at or behind
+    lens[b] read as zeros. Without idx and n: every entry of the table."""
+    _row_type(dtype, "dtype")
+    if idx is not None:
+        if idx.dim() != 2:
+            raise ValueError(f"idx must be [B,n], got {tuple(idx.shape)}")
+        if start is not None:
+            raise ValueError("idx and start exclude each other")
+        if n is not None and n != idx.shape[1]:
+            raise ValueError(f"idx names {idx.shape[1]} entries a sequence, n is {n}")
+        B, n = idx.shape
+    elif block_table is not None:
+        B = block_table.shape[0]
+    else:
+        B = cache.shape[0]
+    code, n_pages, page, D, group, max_pages = _cache_args(cache, scales, block_table, B)
+    n = max_pages * page if n is None else int(n)
+    _want(idx, "idx", torch.int32, (B, n))
+    _want(start, "start", torch.int32, (B,))
+    _want(lens, "lens", torch.int32, (B,))
+    _want(err, "err", torch.int32)
+    dev = cache.device
+    _on(dev, scales=scales, idx=idx, start=start, lens=lens, block_table=block_table, err=err, out=out)
+    if out is None:
+        out = torch.empty((B, n, D), dtype=dtype, device=dev)
+    _want(out, "out", dtype, (B, n, D))
+    st = _call(_lib.sai_q8_cache_read, dev, _ptr(cache), _ptr(scales), _ptr(idx), _ptr(start), _ptr(lens),
+               _ptr(block_table), B, n, D, group, code, n_pages, page, max_pages, _ptr(out), _ROW_TYPES[dtype],
+               _ptr(err))
+    _check(st, "sai_q8_cache_read")
+    return out
+
+
+def q8_quantize(x: torch.Tensor, group: Optional[int] = None, fmt: torch.dtype = torch.int8,
+                codes: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes [...,D], scales [...,D/group]) of x [...,D]: sai_q8_cache_write
+    into a cache that has x's own layout. group None: one scale a row. The
+    codes and scales of an indexer's queries, and the 8-bit activations that
+    indexer_scores_backward reads."""
+    if fmt not in _CODES:
+        raise TypeError(f"fmt must be torch.int8 or torch.float8_e4m3fn, got {fmt}")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must hold rows, got {tuple(x.shape)}")
+    D = x.shape[-1]
+    group = D if group is None else int(group)
+    if group < 1 or D % group:
+        raise ValueError(f"group must divide D = {D}, got {group}")
+    lead = tuple(x.shape[:-1])
+    if codes is None:
+        codes = torch.empty(lead + (D,), dtype=fmt, device=x.device)
+    if scales is None:
+        scales = torch.empty(lead + (D // group,), dtype=torch.float32, device=x.device)
+    _want(codes, "codes", fmt, lead + (D,))
+    _want(scales, "scales", torch.float32, lead + (D // group,))
+    n = lead[-1] if lead else 1
+    try:
+        rows = x.view(-1, n, D)
+    except RuntimeError:
+        raise ValueError("x's leading dimensions must collapse to two strides (a contiguous x does)") from None
+    q8_cache_write(rows, codes.view(-1, n, D), scales.view(-1, n, D // group))
+    return codes, scales
+
+
+def _index_inputs(q8, q_scale, w):
+    """Checked 8-bit queries: (B, S, H, D)."""
+    if q8.dim() != 4:
+        raise ValueError(f"q8 must be [B,S,H,D], got {tuple(q8.shape)}")
+    B, S, H, D = q8.shape
+    _want(q8, "q8", torch.int8)
+    if tuple(q_scale.shape) not in ((B, S, H), (B, S, H, 1)):
+        raise ValueError(f"q_scale must be [B,S,H] (one scale a row), got {tuple(q_scale.shape)}")
+    _want(q_scale, "q_scale", torch.float32)
+    _want(w, "w", torch.float32, (B, S, H))
+    return B, S, H, D
+
+
+def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cache: torch.Tensor,
+                   k_scale: torch.Tensor, cr: int, P: Optional[int] = None,
+                   block_table: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                   k_len: Optional[torch.Tensor] = None, doc_start: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scores [B,S,P] of every candidate block through sai_indexer_scores, -inf
+    elsewhere: indexer_topk's input. q8 [B,S,H,D] int8 with q_scale [B,S,H]
+    (q8_quantize), w [B,S,H] fp32; cache [n_pages,page,D] int8 with k_scale
+    [n_pages,page] (q8_cache_write, one scale a row; without a block_table
+    [B,P,D] and [B,P]). P None: every entry of the table. Decoding: S = 1,
+    q_start the tokens' positions, k_len the entries each cache holds."""
+    B, S, H, D = _index_inputs(q8, q_scale, w)
+    if k_scale.dim() == 2:
+        k_scale = k_scale.unsqueeze(2)
+    code, n_pages, page, Dk, group, max_pages = _cache_args(cache, k_scale, block_table, B)
+    if code != 0:
+        raise TypeError("cache must be int8")
+    if Dk != D or group != D:
+        raise ValueError(f"cache must hold keys of D = {D} with one scale each")
+    if block_table is None and n_pages != B:
+        raise ValueError(f"cache must be [B,P,D] with B = {B} without a block_table, got {tuple(cache.shape)}")
+    P = max_pages * page if P is None else int(P)
+    _want(q_start, "q_start", torch.int32, (B,))
+    _want(k_len, "k_len", torch.int32, (B,))
+    _want(doc_start, "doc_start", torch.int32, (B, S))
+    _want(err, "err", torch.int32)
+    dev = q8.device
+    _on(dev, q_scale=q_scale, w=w, cache=cache, k_scale=k_scale, block_table=block_table, q_start=q_start,
+        k_len=k_len, doc_start=doc_start, out=out, err=err)
+    if out is None:
+        out = torch.empty((B, S, P), dtype=torch.float32, device=dev)
+    _want(out, "out", torch.float32, (B, S, P))
+    st = _call(_lib.sai_indexer_scores, dev, _ptr(q8), _ptr(q_scale), _ptr(w), _ptr(cache), _ptr(k_scale),
+               _ptr(block_table), _ptr(q_start), _ptr(k_len), _ptr(doc_start), B, S, H, D, P, n_pages, page,
+               max_pages, int(cr), _ptr(out), _ptr(err))
+    _check(st, "sai_indexer_scores")
+    return out
+
+
+def scores_backward_workspace_bytes(B: int, S: int, H: int, D: int, P: int, device=None) -> int:
+    """Bytes of scratch that sai_indexer_scores_backward needs on `device`."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        return int(_lib.sai_indexer_scores_backward_workspace_bytes(B, S, H, D, P))
+
+
+def indexer_scores_backward(dscores: torch.Tensor, idx: Optional[torch.Tensor], q8: torch.Tensor,
+                            q_scale: torch.Tensor, w: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tensor, cr: int,
+                            t_begin: int = 0, doc_start: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                            dk: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                            err: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq [B,S,H,D] bf16, dk [B,P,D] bf16, dw [B,S,H] fp32) through
+    sai_indexer_scores_backward: the gradients of indexer_scores with respect
+    to the queries, keys and head weights, given dscores [B,S,K] on the
+    selected blocks idx [B,S,K] (distill_kl's and indexer_topk's outputs; idx
+    None: dscores [B,S,P] on every block). q8, q_scale, k8 [B,P,D] and k_scale
+    [B,P] are the forward's codes, its activation checkpoints."""
+    B, S, H, D = _index_inputs(q8, q_scale, w)
+    if k8.dim() != 3 or k8.shape[0] != B or k8.shape[2] != D:
+        raise ValueError(f"k8 must be [B,P,D] with B = {B}, D = {D}, got {tuple(k8.shape)}")
+    P = k8.shape[1]
+    _want(k8, "k8", torch.int8)
+    if tuple(k_scale.shape) not in ((B, P), (B, P, 1)):
+        raise ValueError(f"k_scale must be [B,P], got {tuple(k_scale.shape)}")
+    _want(k_scale, "k_scale", torch.float32)
+    K = P if idx is None else idx.shape[-1]
+    _want(dscores, "dscores", torch.float32, (B, S, K))
+    _want(idx, "idx", torch.int32, (B, S, K))
+    _want(doc_start, "doc_start", torch.int32, (B, S))
+    _want(err, "err", torch.int32)
+    dev = q8.device
+    need = scores_backward_workspace_bytes(B, S, H, D, P, dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _want(workspace, "workspace", torch.uint8)
+    if dq is None:
+        dq = torch.empty((B, S, H, D), dtype=torch.bfloat16, device=dev)
+    if dk is None:
+        dk = torch.empty((B, P, D), dtype=torch.bfloat16, device=dev)
+    if dw is None:
+        dw = torch.empty((B, S, H), dtype=torch.float32, device=dev)
+    _want(dq, "dq", torch.bfloat16, (B, S, H, D))
+    _want(dk, "dk", torch.bfloat16, (B, P, D))
+    _want(dw, "dw", torch.float32, (B, S, H))
+    _on(dev, dscores=dscores, idx=idx, q_scale=q_scale, w=w, k8=k8, k_scale=k_scale, doc_start=doc_start,
+        workspace=workspace, dq=dq, dk=dk, dw=dw, err=err)
+    st = _call(_lib.sai_indexer_scores_backward, dev, _ptr(dscores), _ptr(idx), _ptr(q8), _ptr(q_scale), _ptr(w),
+               _ptr(k8), _ptr(k_scale), _ptr(doc_start), B, S, H, D, P, K, int(cr), int(t_begin), _ptr(dq), _ptr(dk),
+               _ptr(dw), _ptr(workspace), workspace.numel(), _ptr(err))
+    _check(st, "sai_indexer_scores_backward")
+    return dq, dk, dw
+
+
+def indexer_distill_step(qi: torch.Tensor, w: torch.Tensor, ki: torch.Tensor, Q, Kw, pool, *, K: int, W: int,
+                         cr: int, scale: float, coeff: float, sink=None, doc_start=None, err=None):
+    """One training step of the indexer on the current stream, from its own
+    queries qi [B,S,H,D], keys ki [B,S/cr,D] (bf16, fp16 or fp32) and head
+    weights w [B,S,H] to their gradients: q8_quantize -> indexer_scores ->
+    indexer_topk -> distill_loss -> indexer_scores_backward. Only the 8-bit
+    codes of qi and ki are kept between the two directions. Returns
+    (loss, dq, dk, dw)."""
+    q8, qs = q8_quantize(qi)
+    k8, ks = q8_quantize(ki)
+    scores = indexer_scores(q8, qs, w, k8, ks, cr, doc_start=doc_start, err=err)
+    idx, sel, valid = indexer_topk(scores, cr, K, doc_start=doc_start)
+    loss, ds, _, _ = distill_loss(Q, Kw, pool, idx, sel, valid, W=W, cr=cr, scale=scale, coeff=coeff, sink=sink,
+                                  doc_start=doc_start, err=err)
+    dq, dk, dw = indexer_scores_backward(ds, idx, q8, qs, w, k8, ks, cr, doc_start=doc_start, err=err)
+    return loss, dq, dk, dw

@@ -2,8 +2,6 @@
 // validation, kernel selection by shape, TMA descriptor encoding and launch.
 // Nothing here allocates device memory or synchronises the stream.
 #include <algorithm>
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -11,45 +9,18 @@
 
 #include "sai.h"
 #include "indexer_topk.h"
+#include "sai_host.h"
 #include "sai_kernels.h"
 
 namespace {
 
+using sai::al16;
+using sai::al4;
+using sai::cuda_status;
+using sai::encode_fn;
 using sai::KlPlan;
-
-int sm_count()
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return 0;
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
-int max_smem_optin()
-{
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
+using sai::max_smem_optin;
+using sai::sm_count;
 
 // bf16 matrix [rows, cols] (row-major), box = box_rows x 64 columns, 128-byte
 // swizzle (the layout the tcgen05 descriptors expect).
@@ -68,12 +39,7 @@ bool make_map_bf16(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols
     return r == CUDA_SUCCESS;
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 bool tc_heads(int H) { return H == 16 || H == 32 || H == 64 || H == 128; }
-
-sai_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SAI_OK : SAI_ERR_CUDA; }
 
 }  // namespace
 
