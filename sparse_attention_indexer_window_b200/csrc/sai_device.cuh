@@ -117,6 +117,37 @@ __device__ __forceinline__ bool warp_mbar_wait(uint64_t *bar, uint32_t parity, v
     return __all_sync(0xffffffffu, ok);
 }
 
+// warp_mbar_wait for kernels whose waits are short and many (a tile of a few
+// hundred nanoseconds): the clock, whose read costs as much as such a wait, is
+// read only once a wait has lasted 32 tries. The same limit and outcome.
+__device__ __forceinline__ bool warp_mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                                     int32_t *err)
+{
+    bool ok = true;
+    if (!mbar_try_wait(bar, parity)) {
+        uint64_t t0 = 0;
+        for (uint32_t it = 1; !mbar_try_wait_sleep(bar, parity, kWaitSleepNs); ++it) {
+            if ((it & 31u) != 0)
+                continue;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0)
+                t0 = now;
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            if (now - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                if (err)
+                    atomicExch(err, kErrTimeout);
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Bounded wait used only while unwinding after an abort (short limit, no
 // error reporting): lets in-flight copies land before the CTA exits.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
@@ -149,6 +180,17 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+// 4-byte form, for words whose rows have no wider alignment.
+__device__ __forceinline__ void cp_async4(uint32_t dst_smem, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+// One of the barrier's expected arrivals, made once this thread's cp.async
+// copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -225,6 +267,55 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr)
     d |= (uint64_t)1 << 46;                    // descriptor version (sm_100)
     d |= (uint64_t)2 << 61;                    // 128-byte swizzle
     return d;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, signed 8-bit integers, 32-bit
+// integer accumulate.
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: kind::i8 with signed A/B, s32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N)
+{
+    return (2u << 4)                               // D format: s32
+           | (1u << 7)                             // A format: signed
+           | (1u << 10)                            // B format: signed
+           | ((uint32_t)(N >> 3) << 17)            // N / 8
+           | ((uint32_t)(M >> 4) << 24);           // M / 16
+}
+
+// Shared-memory matrix descriptor for a K-major operand whose rows are as long
+// as its swizzle span (32, 64 or 128 bytes), packed in 8-row atoms.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint64_t sdesc_k_rows(uint32_t saddr)
+{
+    constexpr uint64_t layout = ROW_BYTES == 128 ? 2 : (ROW_BYTES == 64 ? 4 : 6);
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);          // start address
+    d |= (uint64_t)1 << 16;                            // leading byte offset (unused here)
+    d |= (uint64_t)((8 * ROW_BYTES) >> 4) << 32;       // stride byte offset: 8 rows
+    d |= (uint64_t)1 << 46;                            // descriptor version (sm_100)
+    d |= layout << 61;
+    return d;
+}
+
+// 3-D tiled load of the map's box at element coordinates (x, y, z) into smem.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x,
+                                            int32_t y, int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
 // 32 lanes x 16 columns of 32-bit TMEM words into registers (one lane per
