@@ -2,6 +2,7 @@
 // (q8_cache.cu), the indexer's scores (indexer_scores.cu) and their gradient
 // (indexer_scores_bwd.cu). Not part of the public ABI.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -64,6 +65,12 @@ struct ScoresArgs {
     int32_t *err;
 };
 cudaError_t launch_indexer_scores(const ScoresArgs &a, cudaStream_t stream);
+
+// TMA map of 8-bit rows [d2][d1][d0], box d0 x box1 x box2, swizzled over its
+// rows; and H rounded up to the power of two that the tensor-core tiles take.
+bool make_map_q8(CUtensorMap *m, const void *ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,
+                 uint32_t box2);
+int padded_heads(int H);
 
 struct ScoresBwdArgs {
     const float *dscores;    // [B,S,K]

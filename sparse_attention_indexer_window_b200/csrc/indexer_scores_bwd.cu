@@ -1,158 +1,965 @@
 // Gradient of the indexer's scores from the 8-bit codes that the forward kept
-// (its activation checkpoints). With G[t,j] the gradient of s[t,j] summed over
-// the slots that select block j (0 where nothing does or j is no candidate),
-// and m[t,h,j] = 1 where <q8[t,h], k8[j]> > 0 (relu's derivative, exact since
-// the products of codes are whole numbers):
+// (its activation checkpoints), on tcgen05 tensor cores (sm_100a). With G[t,j]
+// the gradient of s[t,j] summed over the slots that select block j (0 where
+// nothing does or j is no candidate), and m[t,h,j] = 1 where <q8[t,h], k8[j]> > 0
+// (relu's derivative, exact since the products of codes are whole numbers):
 //
 //   dq[t,h,:] = w[t,h] sum_j m G[t,j] ks[j] k8[j,:]
 //   dk[j,:]   = sum_{t,h} m G[t,j] w[t,h] qs[t,h] q8[t,h,:]
 //   dw[t,h]   = qs[t,h] sum_j G[t,j] ks[j] relu(<q8[t,h], k8[j]>)
 //
-// the gradients with respect to the values that the codes stand for. An entry
-// with G = 0 contributes nothing, whatever its scale holds.
+// the gradients with respect to the values that the codes stand for.
 //
-// Three launches: G written out densely, dq and dw by token, dk by block.
+// Launches: bwd_prep_kernel writes G densely (slots of one block added in slot
+// order) with the largest magnitudes; bwd_tc_kernel<dq> and <dk>; and
+// bwd_reduce_kernel adds dk's partial sums in a fixed order. Nothing depends on
+// timing: the same inputs give the same bits.
+//
+// Both tensor-core kernels have one form. Two stationary 128-row tiles A (query
+// rows for dq, keys for dk) meet a stream of 128-row tiles B (keys; query
+// rows). Each step forms S = A B^T in 8-bit integers (kind::i8, exact), the
+// epilogue turns S in place into M, fp16, the masked gradient of each product,
+// and M, read from tensor memory as the A operand, multiplies B's codes in fp16
+// (whole numbers up to 127 are exact there) into an fp32 accumulator:
+//
+//   dq: lanes are (t,h) rows; M = m gk, gk[t,j] = G[t,j] ks[j]; B2 = k8. The
+//       fp32 sum for dw runs beside it. gk comes from shared memory, the same
+//       for all heads of a token.
+//   dk: lanes are keys; M = m G[t,j], one value a lane and token; B2 =
+//       w qs q8, scaled by row as the codes are turned into fp16.
+//
+// fp16's 11 bits (a rounding of 2^-11 of each term, below the bf16 outputs'
+// 2^-8) hold the operands after one common power of two brings the largest to
+// the top of its range; what falls out at the other end is below 2^-39 of it.
+//
+// Bound: per 128 x 128 tile of D = 128, 256 cycles of kind::i8 and 512 of
+// kind::f16 on the tensor pipe. The two stationary tiles alternate: while one's
+// M is formed the other's products run. Warp roles (512 threads): warp 0 TMA,
+// warp 1 MMA issue, warps 4..7 and 8..11 the epilogues of the two tiles, warps
+// 12..15 turn B's codes into fp16. Every wait is bounded; on timeout the kernel
+// records SAI_ERR_TIMEOUT and unwinds.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
 
 #include "indexer_q8.h"
 #include "sai_device.cuh"
+#include "sai_host.h"
 
 namespace sai {
 namespace {
 
-__device__ __forceinline__ bool candidate(const ScoresBwdArgs &a, int64_t row, int t, int j)
+constexpr int kBwThreads = 512;
+constexpr int kBwRing = 3;              // code tiles B in flight
+constexpr int kBwMaxTok = 16;           // tokens of a 128-row tile (HP = 8)
+constexpr int kBwRow = 132;             // floats between two tokens' staged gk (4 more than a tile: no bank conflicts)
+constexpr int kPrepThreads = 256;
+constexpr int kPrepCols = 4096;         // columns of G gathered at once
+
+// Largest magnitudes, as bits: |G ks|, |G|, |w qs| of tokens with a gradient.
+enum { kMaxGk = 0, kMaxG = 1, kMaxW = 2, kMaxWords = 4 };
+
+struct BwPlan {
+    int tt;                // tokens a 128-row tile
+    int n_steps_seq;       // dk: token tiles a sequence
+    int n_pairs;           // dk: 256-key pairs a sequence; dq: token pairs (2 tt tokens) a sequence
+    long long total;       // dk: steps of the whole batch
+    const float *G;        // [B,S,P]
+    const uint32_t *max;   // kMaxWords
+    const uint32_t *row;   // [B,S] not 0 where the token has a gradient
+    float *part;           // dk: [grid + B n_pairs][256][D]
+};
+
+// The power of two that brings a largest magnitude (bits) below 2^top, at
+// least half way; 1 when there is none or it is not finite.
+__device__ __forceinline__ float range_scale(uint32_t bits, int top)
+{
+    if (bits == 0u || bits >= 0x7f800000u)
+        return 1.f;
+    int e;
+    frexpf(__uint_as_float(bits), &e);            // magnitude in [2^(e-1), 2^e)
+    return ldexpf(1.f, max(-120, min(120, top - e)));
+}
+
+// Candidates [lo, hi) of the token at local index t.
+__device__ __forceinline__ void token_range(const ScoresBwdArgs &a, int b, int t, int &lo, int &hi)
 {
     const int64_t pos = (int64_t)a.t_begin + t;
-    int64_t d0 = a.doc_start ? __ldg(a.doc_start + row) : 0;
+    int64_t d0 = a.doc_start ? (int64_t)__ldg(a.doc_start + (int64_t)b * a.S + t) : 0;
     d0 = d0 < 0 ? 0 : (d0 > pos ? pos : d0);
-    return (int64_t)(j + 1) * a.cr - 1 <= pos && (int64_t)j * a.cr >= d0;
+    hi = (int)min((int64_t)a.P, (pos + 1) / a.cr);
+    lo = (int)min((int64_t)hi, (d0 + a.cr - 1) / a.cr);
 }
 
-// One block per token. Slots that name the same block are added in slot order
-// by the one thread that owns the block, so the sum does not depend on timing.
-__global__ void __launch_bounds__(256) bwd_scatter_kernel(const ScoresBwdArgs a, float *G)
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *buf)
 {
-    const int64_t row = blockIdx.x;
-    const int t = (int)(row % a.S);
-    float *g = G + row * a.P;
-    for (int j = threadIdx.x; j < a.P; j += 256)
-        g[j] = a.idx ? 0.f : (candidate(a, row, t, j) ? a.dscores[row * a.P + j] : 0.f);
-    if (!a.idx)
-        return;
+    v = __reduce_max_sync(0xffffffffu, v);
     __syncthreads();
-    for (int k = 0; k < a.K; ++k) {
-        const int j = __ldg(a.idx + row * a.K + k);
-        if (j < -1 || j >= a.P) {
-            if (threadIdx.x == 0 && a.err)
+    if ((threadIdx.x & 31) == 0)
+        buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = buf[threadIdx.x & (kPrepThreads / 32 - 1)];
+    return __reduce_max_sync(0xffffffffu, v);
+}
+
+// One block a token. With idx: the token's G, gathered in shared memory
+// kPrepCols columns at a time and written out where it has candidates.
+// Slots of one block: two are added in either order to the same bits; a third
+// one (a counter a block notices it) has the columns gathered again by one
+// thread a block in slot order.
+__global__ void __launch_bounds__(kPrepThreads)
+    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any)
+{
+    __shared__ float g[kPrepCols];
+    __shared__ uint32_t cnt[kPrepCols / 4];
+    __shared__ uint32_t buf[kPrepThreads / 32];
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / a.S);
+    const int t = (int)(row - (int64_t)b * a.S);
+    int lo, hi;
+    token_range(a, b, t, lo, hi);
+    uint32_t any = 0, top_g = 0, top_gk = 0;
+    // the largest finite magnitude: one NaN or infinity does not unscale the others
+    auto finite = [](float v) {
+        const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+        return u < 0x7f800000u ? u : 0u;
+    };
+    const float *ks = a.k_scale + (int64_t)b * a.P;
+    const float *ds = a.dscores + row * a.K;
+    auto seen = [&](float v, int j) {
+        if (v != 0.f) {
+            any = 1u;
+            top_g = max(top_g, finite(v));
+            top_gk = max(top_gk, finite(v * __ldg(ks + j)));
+        }
+    };
+    if (!a.idx) {
+        for (int j = lo + threadIdx.x; j < hi; j += kPrepThreads)
+            seen(__ldg(ds + j), j);
+    } else {
+        const int32_t *idx = a.idx + row * a.K;
+        for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
+            const int j = __ldg(idx + k);
+            if ((j < -1 || j >= a.P) && a.err)
                 atomicExch(a.err, kErrIndex);
-        } else if (j >= 0 && (j & 255) == (int)threadIdx.x && candidate(a, row, t, j)) {
-            g[j] += a.dscores[row * a.K + k];
+        }
+        for (int c0 = lo / 4 * 4; c0 < hi; c0 += kPrepCols) {
+            const int n = min(kPrepCols, hi - c0);
+            for (int j = threadIdx.x; j < n; j += kPrepThreads)
+                g[j] = 0.f;
+            for (int j = threadIdx.x; j < (n + 3) / 4; j += kPrepThreads)
+                cnt[j] = 0u;
+            __syncthreads();
+            bool third = false;
+            for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
+                const int id = __ldg(idx + k), j = id - c0;
+                if (id < lo || id >= hi || j < 0 || j >= n)
+                    continue;
+                atomicAdd(&g[j], __ldg(ds + k));
+                const uint32_t old = atomicAdd(&cnt[j >> 2], 1u << (8 * (j & 3)));
+                third |= ((old >> (8 * (j & 3))) & 255u) >= 2u;
+            }
+            if (__syncthreads_or(third)) {
+                for (int j = threadIdx.x; j < n; j += kPrepThreads)
+                    g[j] = 0.f;
+                __syncthreads();
+                for (int k = 0; k < a.K; ++k) {
+                    const int id = __ldg(idx + k), j = id - c0;
+                    if (id >= lo && id < hi && j >= 0 && j < n && (j & (kPrepThreads - 1)) == (int)threadIdx.x)
+                        g[j] += __ldg(ds + k);
+                }
+                __syncthreads();
+            }
+            for (int j = threadIdx.x; j < n; j += kPrepThreads) {
+                const float v = g[j];
+                if (c0 + j >= lo)
+                    G[row * a.P + c0 + j] = v;
+                seen(v, c0 + j);
+            }
+            __syncthreads();
         }
     }
-}
-
-__device__ __forceinline__ int dot_codes(const int8_t *x, const int8_t *y, int D)
-{
-    int dot = 0;
-    for (int i = 0; i < D / 16; ++i) {
-        const int4 p = reinterpret_cast<const int4 *>(x)[i], q = reinterpret_cast<const int4 *>(y)[i];
-        dot = __dp4a(p.x, q.x, dot);
-        dot = __dp4a(p.y, q.y, dot);
-        dot = __dp4a(p.z, q.z, dot);
-        dot = __dp4a(p.w, q.w, dot);
+    any = block_max(any, buf);
+    if (threadIdx.x == 0)
+        row_any[row] = any;
+    if (any == 0u)
+        return;
+    top_g = block_max(top_g, buf);
+    top_gk = block_max(top_gk, buf);
+    uint32_t top_w = 0;
+    for (int h = threadIdx.x; h < a.H; h += kPrepThreads)
+        top_w = max(top_w, finite(a.w[row * a.H + h] * a.q_scale[row * a.H + h]));
+    top_w = block_max(top_w, buf);
+    if (threadIdx.x < 3) {
+        const uint32_t v = threadIdx.x == kMaxGk ? top_gk : (threadIdx.x == kMaxG ? top_g : top_w);
+        // (a stale word only means one more atomic)
+        if (v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
+            atomicMax(gmax + threadIdx.x, v);
     }
-    return dot;
 }
 
-// One block per (token, head): thread d owns dq[d]; 128 keys at a time.
-__global__ void __launch_bounds__(128) bwd_q_kernel(const ScoresBwdArgs a, const float *G)
+// ------------------------------------------------------------ the walk
+// The steps of one CTA, the same for every role: dq walks items blockIdx.x,
+// + gridDim.x, ... (2 tt tokens each, late tokens first) and their key tiles;
+// dk walks a contiguous share of all steps of the batch (a pair of key tiles
+// times the token tiles that see it), so its share may end inside a pair.
+template <int MODE>
+struct Walk {
+    int b, a0;          // sequence; the stationary rows' first token (dq) or key (dk)
+    int s, s_end;       // the streamed tile and the end of the item's
+    bool first;         // the item's first step
+    int pair;           // dk: pair of the batch
+    // position
+    int item;
+    long long at, end;
+
+    __device__ __forceinline__ bool set(const ScoresBwdArgs &a, const BwPlan &p);
+    __device__ __forceinline__ bool begin(const ScoresBwdArgs &a, const BwPlan &p)
+    {
+        item = (int)blockIdx.x;
+        at = p.total * blockIdx.x / gridDim.x;
+        end = p.total * (blockIdx.x + 1) / gridDim.x;
+        return set(a, p);
+    }
+    __device__ __forceinline__ bool next(const ScoresBwdArgs &a, const BwPlan &p)
+    {
+        first = false;
+        if (++s < s_end)
+            return true;
+        if (MODE == 0)
+            item += gridDim.x;
+        return set(a, p);
+    }
+    __device__ __forceinline__ bool last() const { return s == s_end - 1; }
+};
+
+// First token tile that sees a key of pair kp.
+__device__ __forceinline__ int first_step(const ScoresBwdArgs &a, const BwPlan &p, int kp)
 {
-    __shared__ float m[128];
-    __shared__ float part[4];
-    const int64_t rh = blockIdx.x;
-    const int64_t row = rh / a.H;
-    const int b = (int)(row / a.S);
-    const int8_t *q = a.q8 + rh * a.D;
-    const int8_t *kb = a.k8 + (int64_t)b * a.P * a.D;
-    float acc = 0.f, dw = 0.f;
-    for (int j0 = 0; j0 < a.P; j0 += 128) {
-        const int j = j0 + threadIdx.x;
-        float v = 0.f;
-        if (j < a.P) {
-            const float g = G[row * a.P + j];
-            if (g != 0.f) {
-                const float gk = g * a.k_scale[(int64_t)b * a.P + j];
-                const int dot = dot_codes(q, kb + (int64_t)j * a.D, a.D);
-                dw += gk * (float)max(dot, 0);
-                v = dot > 0 ? gk : 0.f;
+    const int64_t t = (int64_t)(256 * (int64_t)kp + 1) * a.cr - 1 - a.t_begin;
+    return t <= 0 ? 0 : (int)min((int64_t)p.n_steps_seq, t / p.tt);
+}
+
+template <>
+__device__ __forceinline__ bool Walk<0>::set(const ScoresBwdArgs &a, const BwPlan &p)
+{
+    for (; item < a.B * p.n_pairs; item += gridDim.x) {
+        b = item % a.B;
+        a0 = (p.n_pairs - 1 - item / a.B) * 2 * p.tt;
+        const int64_t t_last = min(a.S, a0 + 2 * p.tt) - 1;
+        s = 0;
+        s_end = (int)((min((int64_t)a.P, ((int64_t)a.t_begin + t_last + 1) / a.cr) + 127) / 128);
+        first = true;
+        if (s_end > 0)
+            return true;
+        // no candidate: the epilogue's roles write the zeros (see zero_item)
+    }
+    return false;
+}
+
+template <>
+__device__ __forceinline__ bool Walk<1>::set(const ScoresBwdArgs &a, const BwPlan &p)
+{
+    if (at >= end)
+        return false;
+    const long long per_seq = p.total / a.B;
+    b = (int)(at / per_seq);
+    long long r = at - b * per_seq;
+    int kp = 0, f = first_step(a, p, 0);
+    while (r >= p.n_steps_seq - f) {
+        r -= p.n_steps_seq - f;
+        f = first_step(a, p, ++kp);
+    }
+    s = f + (int)r;
+    const long long n = min((long long)(p.n_steps_seq - s), end - at);
+    s_end = s + (int)n;
+    at += n;
+    a0 = kp * 256;
+    pair = b * p.n_pairs + kp;
+    first = true;
+    return true;
+}
+
+struct BwSmem {
+    uint64_t a_full[2], a_empty[2];
+    uint64_t b_full[kBwRing], b_empty[kBwRing];
+    uint64_t c_full[2], c_empty[2];      // fp16 tiles
+    uint64_t s_full[2], m_full[2];       // per stationary tile: products there; M there
+    uint64_t acc_full[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int lo[2][kBwMaxTok], hi[2][kBwMaxTok];        // dq: the tokens' candidates, per tile
+};
+
+template <int D>
+constexpr size_t bw_smem_bytes(bool dq)
+{
+    return 1024 + 4 * 128 * D + (size_t)kBwRing * 128 * D + 2 * 128 * D * 2 +
+           (dq ? 2 * 2 * (size_t)kBwMaxTok * kBwRow * 4 : 0) + sizeof(BwSmem);
+}
+
+// Offset of 16-byte chunk c of row r in a tile of ROW_BYTES rows stored with
+// the swizzle of that span (rows of 32, 64 or 128 bytes; the 16-byte chunks
+// of a row are permuted by the row's place in its 8-row atom).
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c)
+{
+    if (ROW_BYTES == 128)
+        c ^= r & 7u;
+    else if (ROW_BYTES == 64)
+        c ^= (r >> 1) & 3u;
+    else
+        c ^= (r >> 2) & 1u;
+    return r * ROW_BYTES + c * 16;
+}
+
+template <int MODE, int D, int HP>
+__global__ void __launch_bounds__(kBwThreads, 1)
+    bwd_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+                  const ScoresBwdArgs a, const BwPlan p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int TT = 128 / HP;                       // tokens of a 128-row tile
+    constexpr uint32_t tile8 = 128 * D, tile16 = 256 * D;
+    constexpr int kC = D * 2 > 128 ? 128 : D * 2;      // bytes of a row block of the fp16 tile
+    uint8_t *sa = base;                                // [2 items][2 tiles]
+    uint8_t *sb = sa + 4 * tile8;                      // [ring]
+    uint8_t *sc = sb + kBwRing * tile8;                // [2] fp16
+    float *sg = reinterpret_cast<float *>(sc + 2 * tile16);   // dq: [2 tiles][2][kBwMaxTok][kBwRow] gk
+    BwSmem *sm = reinterpret_cast<BwSmem *>(reinterpret_cast<uint8_t *>(sg) +
+                                            (MODE == 0 ? 4 * kBwMaxTok * kBwRow * 4 : 0));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->a_full[i], 1);
+            mbar_init(&sm->a_empty[i], 1);
+            mbar_init(&sm->c_full[i], 4);
+            mbar_init(&sm->c_empty[i], 1);
+            mbar_init(&sm->s_full[i], 1);
+            mbar_init(&sm->m_full[i], 4);
+            mbar_init(&sm->acc_full[i], 1);
+        }
+        for (int i = 0; i < kBwRing; ++i) {
+            mbar_init(&sm->b_full[i], 1);
+            mbar_init(&sm->b_empty[i], 1 + 4);
+        }
+        mbar_init(&sm->drain, 1);
+        sm->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;               // S/M of the two tiles, then their accumulators
+    volatile int *abort_flag = &sm->abort_flag;
+    Walk<MODE> wk;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            tma_prefetch_desc(&mapA);
+            tma_prefetch_desc(&mapB);
+        }
+        int stage = 0, item = -1;
+        uint32_t phase = 0, a_used = 0, b_used = 0, b_parity = 0;
+        bool ok = true;
+        for (bool go = wk.begin(a, p); go; go = wk.next(a, p)) {
+            if (wk.first) {
+                ++item;
+                const int ab = item & 1;
+                if (!warp_mbar_wait_short(&sm->a_empty[ab], ((item >> 1) & 1) ^ 1u, abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm->a_full[ab], 2 * tile8);
+                    for (int i = 0; i < 2; ++i) {
+                        uint8_t *dst = sa + (2 * ab + i) * tile8;
+                        if (MODE == 0)
+                            tma_load_3d(dst, &mapA, &sm->a_full[ab], 0, 0, wk.b * a.S + wk.a0 + i * TT);
+                        else
+                            tma_load_3d(dst, &mapA, &sm->a_full[ab], 0, wk.a0 + i * 128, wk.b);
+                    }
+                }
+                __syncwarp();
+                a_used |= 1u << ab;
+            }
+            if (!warp_mbar_wait_short(&sm->b_empty[stage], phase ^ 1u, abort_flag, a.err)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm->b_full[stage], tile8);
+                if (MODE == 0)
+                    tma_load_3d(sb + stage * tile8, &mapB, &sm->b_full[stage], 0, wk.s * 128, wk.b);
+                else
+                    tma_load_3d(sb + stage * tile8, &mapB, &sm->b_full[stage], 0, 0, wk.b * a.S + wk.s * TT);
+            }
+            __syncwarp();
+            b_used |= 1u << stage;
+            b_parity = (b_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == kBwRing) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
-        m[threadIdx.x] = v;
-        __syncthreads();
-        if ((int)threadIdx.x < a.D)
-            for (int i = 0; i < min(128, a.P - j0); ++i)
-                if (m[i] != 0.f)
-                    acc += m[i] * (float)kb[(int64_t)(j0 + i) * a.D + threadIdx.x];
-        __syncthreads();
-    }
+        if (!ok && lane == 0) {
+            // let the copies in flight land before the CTA goes
+            for (int i = 0; i < kBwRing; ++i)
+                if (b_used & (1u << i))
+                    mbar_drain(&sm->b_full[i], (b_parity >> i) & 1u);
+            for (int i = 0; i < 2; ++i)
+                if (a_used & (1u << i)) {
+                    const int uses = (item - i + 2) / 2;       // loads asked for into buffer i, or one more
+                    mbar_drain(&sm->a_full[i], (uint32_t)(uses - 1) & 1u);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t id_s = idesc_i8_s32(128, 128);
+        constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
+        int stage = 0, item = -1, n = 0;
+        uint32_t phase = 0;
+        bool ok = true, issued = false;
+        auto products = [&](int i) {
+            // S_i = A_i B^T of the walk's step (lane 0)
+            const uint64_t da = sdesc_k_rows<D>(smem_u32(sa + (2 * (item & 1) + i) * tile8));
+            const uint64_t db = sdesc_k_rows<D>(smem_u32(sb + stage * tile8));
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        dw += __shfl_xor_sync(0xffffffffu, dw, o);
-    if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = dw;
+            for (int kk = 0; kk < D / 32; ++kk)
+                umma_i8(tmem + i * 128, da + 2 * kk, db + 2 * kk, id_s, kk != 0);
+            umma_commit(&sm->s_full[i]);
+        };
+        // the step whose tiles are in place next
+        auto arrive_step = [&]() -> bool {
+            if (wk.first) {
+                ++item;
+                if (!warp_mbar_wait_short(&sm->a_full[item & 1], (item >> 1) & 1, abort_flag, a.err))
+                    return false;
+            }
+            return warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err);
+        };
+        auto done_step = [&]() {
+            // after both tiles' products of the step are issued
+            if (lane == 0) {
+                umma_commit(&sm->b_empty[stage]);
+                if (wk.last())
+                    umma_commit(&sm->a_empty[item & 1]);
+            }
+            __syncwarp();
+            if (++stage == kBwRing) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        bool go = wk.begin(a, p);
+        if (go) {
+            ok = arrive_step();
+            if (ok) {
+                tc_fence_after();
+                if (lane == 0) {
+                    products(0);
+                    products(1);
+                    issued = true;
+                }
+                __syncwarp();
+                done_step();
+            }
+        }
+        while (go && ok) {
+            const bool fresh = wk.first, closes = wk.last();
+            const int cb = n & 1;
+            const uint64_t dc = sdesc_mn_rows<kC>(smem_u32(sc + cb * tile16), 128 * kC);
+            go = wk.next(a, p);                  // the walk is now one step ahead
+            for (int i = 0; i < 2 && ok; ++i) {
+                ok = warp_mbar_wait_short(&sm->m_full[i], n & 1, abort_flag, a.err);
+                if (ok && i == 0) {
+                    ok = warp_mbar_wait_short(&sm->c_full[cb], (n >> 1) & 1, abort_flag, a.err);
+                    if (ok && go)
+                        ok = arrive_step();
+                }
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_f16_ta(tmem + 256 + i * D, tmem + i * 128 + kk * 8, dc + kk * (16 * kC / 16), id_acc,
+                                    (kk != 0 || !fresh) ? 1u : 0u);
+                    if (closes)
+                        umma_commit(&sm->acc_full[i]);
+                    if (i == 1)
+                        umma_commit(&sm->c_empty[cb]);
+                    if (go)
+                        products(i);
+                }
+                __syncwarp();
+            }
+            if (ok && go)
+                done_step();
+            ++n;
+        }
+        if (!ok && lane == 0 && issued) {
+            umma_commit(&sm->drain);
+            mbar_drain(&sm->drain, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 12) {
+        // ------------------------------------------------ codes to fp16
+        const int r = threadIdx.x - 384;               // row of the tile
+        const float fw = MODE == 1 ? range_scale(__ldg(p.max + kMaxW), 8) : 1.f;
+        // dk: this row's scale, loaded a step ahead
+        auto scale_of = [&](int s) -> float {
+            const int tt = r / HP, h = r % HP;
+            const int t = s * TT + tt;
+            if (t >= a.S || h >= a.H)
+                return 0.f;
+            const int64_t row = (int64_t)wk.b * a.S + t;
+            if (__ldg(p.row + row) == 0u)
+                return 0.f;                            // no gradient: whatever w holds, the row adds nothing
+            return __ldg(a.w + row * a.H + h) * __ldg(a.q_scale + row * a.H + h) * fw;
+        };
+        int stage = 0, n = 0;
+        uint32_t phase = 0;
+        bool go = wk.begin(a, p);
+        float scale = MODE == 1 && go ? scale_of(wk.s) : 1.f;
+        while (go) {
+            go = wk.next(a, p);
+            const float next_scale = MODE == 1 && go ? scale_of(wk.s) : 1.f;
+            const int cb = n & 1;
+            if (!warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err) ||
+                !warp_mbar_wait_short(&sm->c_empty[cb], ((n >> 1) & 1) ^ 1u, abort_flag, a.err))
+                break;
+            const uint8_t *src = sb + stage * tile8;
+            uint8_t *dst = sc + cb * tile16;
+            // scale as an fp16 pair whose sum has 22 bits: x * scale is rounded once
+            const __half hi = __float2half_rn(scale);
+            const __half lo = __float2half_rn(scale - __half2float(hi));
+            const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+            const __half2 off = __floats2half2_rn(-1152.f, -1152.f);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + swz<D>(r, c));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // byte x as x + 128 under the exponent of 1024: 1152 + x in fp16, exact
+                    const uint32_t u = w[e] ^ 0x80808080u;
+                    const uint32_t p01 = __byte_perm(u, 0x64646464u, 0x4140), p23 = __byte_perm(u, 0x64646464u, 0x4342);
+                    __half2 h01 = __hadd2(*reinterpret_cast<const __half2 *>(&p01), off);
+                    __half2 h23 = __hadd2(*reinterpret_cast<const __half2 *>(&p23), off);
+                    if (MODE == 1) {
+                        h01 = __hfma2(h01, hi2, __hmul2(h01, lo2));
+                        h23 = __hfma2(h23, hi2, __hmul2(h23, lo2));
+                    }
+                    o[2 * e] = *reinterpret_cast<const uint32_t *>(&h01);
+                    o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h23);
+                }
+                // 16 values are two 16-byte chunks of the row's fp16 block
+                const uint32_t ch = 2 * c, blk = ch / (kC / 16), cc = ch % (kC / 16);
+                uint8_t *d = dst + blk * (128 * kC);
+                *reinterpret_cast<uint4 *>(d + swz<kC>(r, cc)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(d + swz<kC>(r, cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm->c_full[cb]);
+                mbar_arrive(&sm->b_empty[stage]);
+            }
+            scale = next_scale;
+            ++n;
+            if (++stage == kBwRing) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ epilogue of tile i
+        const int i = (warp - 4) >> 2;
+        const int q = warp & 3;
+        const int r = q * 32 + lane;                   // tile row
+        const uint32_t ts = tmem + i * 128 + ((uint32_t)(q * 32) << 16);
+        const uint32_t ta = tmem + 256 + i * D + ((uint32_t)(q * 32) << 16);
+        if constexpr (MODE == 0) {
+            const float f = range_scale(__ldg(p.max + kMaxGk), 15);
+            const float inv = 1.f / f;
+            const int tt = r / HP, h = r % HP;
+            float *stage0 = sg + i * 2 * kBwMaxTok * kBwRow;
+            // Items without a candidate never reach the walk: their gradients are zero.
+            for (int it = (int)blockIdx.x; it < a.B * p.n_pairs; it += gridDim.x) {
+                const int b = it % a.B, t = (p.n_pairs - 1 - it / a.B) * 2 * TT + i * TT + tt;
+                const int64_t t_last = min(a.S, (p.n_pairs - 1 - it / a.B) * 2 * TT + 2 * TT) - 1;
+                if (((int64_t)a.t_begin + t_last + 1) / a.cr > 0 || t >= a.S || h >= a.H)
+                    continue;
+                const int64_t row = ((int64_t)b * a.S + t) * a.H + h;
+                a.dw[row] = 0.f;
+                for (int c = 0; c < D / 8; ++c)
+                    reinterpret_cast<uint4 *>(a.dq + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            // gk of the step's 128 keys and this tile's tokens: thread = key, one value a token
+            float g[TT], ksv = 0.f;
+            auto fetch = [&]() {
+                const int j = wk.s * 128 + r;
+                ksv = j < a.P ? __ldg(a.k_scale + (int64_t)wk.b * a.P + j) : 0.f;
+                const float *src = p.G + ((int64_t)wk.b * a.S + wk.a0 + i * TT) * a.P + j;
+#pragma unroll
+                for (int e = 0; e < TT; ++e)
+                    g[e] = j >= sm->lo[i][e] && j < sm->hi[i][e] ? __ldg(src + (int64_t)e * a.P) : 0.f;
+            };
+            auto bounds = [&]() {
+                named_bar_sync(1 + i, 128);
+                if (r < TT) {
+                    const int t = wk.a0 + i * TT + r;
+                    int lo = 0, hi = 0;
+                    if (t < a.S)
+                        token_range(a, wk.b, t, lo, hi);
+                    sm->lo[i][r] = lo;
+                    sm->hi[i][r] = hi;
+                }
+                named_bar_sync(1 + i, 128);
+            };
+            auto put = [&](int buf) {
+#pragma unroll
+                for (int e = 0; e < TT; ++e)
+                    stage0[(buf * kBwMaxTok + e) * kBwRow + r] = g[e] != 0.f ? g[e] * ksv * f : 0.f;
+            };
+            int n = 0, items = 0;
+            bool go = wk.begin(a, p), ok = true;
+            if (go) {
+                bounds();
+                fetch();
+            }
+            float dw[4] = {0.f, 0.f, 0.f, 0.f};
+            while (go) {
+                put(n & 1);
+                // a wait that gave up ends the loop here, for the four warps together
+                if (!named_bar_and(1 + i, 128, ok))
+                    break;
+                const Walk<MODE> me = wk;
+                const bool closes = wk.last();
+                go = wk.next(a, p);
+                if (go) {
+                    if (wk.first)
+                        bounds();
+                    fetch();                            // the next step's, in flight during this one
+                }
+                if (!warp_mbar_wait_short(&sm->s_full[i], n & 1, abort_flag, a.err)) {
+                    ok = false;
+                    continue;
+                }
+                tc_fence_after();
+                const float *gk = stage0 + ((n & 1) * kBwMaxTok + tt) * kBwRow;
+                uint32_t x[2][16];
+                tmem_ld16(ts, x[0]);
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    const uint32_t(&v)[16] = x[(c / 16) & 1];
+                    tmem_ld_wait();
+                    if (c + 16 < 128)
+                        tmem_ld16(ts + c + 16, x[(c / 16 + 1) & 1]);
+                    uint32_t m[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(gk + c + e);
+                        const float wv[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t on[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            on[u] = (uint32_t)__vimin_s32_relu((int)v[e + u], 1);
+                            dw[u] = fmaf(__int_as_float(__viaddmax_s32((int)v[e + u], 0x4B000000, 0x4B000000)) -
+                                             8388608.f,
+                                         wv[u], dw[u]);
+                        }
+                        const __half2 h01 = __floats2half2_rn(w.x, w.y), h23 = __floats2half2_rn(w.z, w.w);
+                        m[e / 2] = *reinterpret_cast<const uint32_t *>(&h01) & ((on[0] + (on[1] << 16)) * 0xffffu);
+                        m[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h23) & ((on[2] + (on[3] << 16)) * 0xffffu);
+                    }
+                    tmem_st8(ts + c / 2, m);            // these columns have been read
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->m_full[i]);
+                ++n;
+                if (closes) {
+                    if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err)) {
+                        ok = false;
+                        continue;
+                    }
+                    ++items;
+                    tc_fence_after();
+                    const int t = me.a0 + i * TT + tt;
+                    const bool mine = t < a.S && h < a.H;
+                    const int64_t trow = (int64_t)me.b * a.S + (mine ? t : 0);
+                    const int64_t row = trow * a.H + (mine ? h : 0);
+                    const bool any = mine && __ldg(p.row + trow) != 0u;
+                    const float wq = any ? __ldg(a.w + row) * inv : 0.f;
+                    if (mine)
+                        a.dw[row] = any ? ((dw[0] + dw[1]) + (dw[2] + dw[3])) * inv * __ldg(a.q_scale + row) : 0.f;
+                    dw[0] = dw[1] = dw[2] = dw[3] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t v[16], o[8];
+                        tmem_ld16(ta + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float y0 = any ? __uint_as_float(v[2 * e]) * wq : 0.f;
+                            const float y1 = any ? __uint_as_float(v[2 * e + 1]) * wq : 0.f;
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
+                            o[e] = *reinterpret_cast<const uint32_t *>(&y);
+                        }
+                        if (mine) {
+                            uint4 *d = reinterpret_cast<uint4 *>(a.dq + row * D + c);
+                            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                    tc_fence_before();
+                }
+            }
+        } else {
+            const float fg = range_scale(__ldg(p.max + kMaxG), 15);
+            const float inv = 1.f / fg, inv_w = 1.f / range_scale(__ldg(p.max + kMaxW), 8);
+            // this key's gradients of the step's tokens, as fp16 bits, loaded a step ahead
+            uint32_t g[TT];
+            float raw[TT];
+            auto fetch = [&]() {
+                const int j = wk.a0 + i * 128 + r;
+                const int t0 = wk.s * TT;
+                int lo = 0, hi = 0;
+                if (lane < TT && t0 + lane < a.S)
+                    token_range(a, wk.b, t0 + lane, lo, hi);
+                const float *src = p.G + ((int64_t)wk.b * a.S + t0) * a.P + j;
+#pragma unroll
+                for (int e = 0; e < TT; ++e) {
+                    const int l = __shfl_sync(0xffffffffu, lo, e), u = __shfl_sync(0xffffffffu, hi, e);
+                    raw[e] = j >= l && j < u ? __ldg(src + (int64_t)e * a.P) : 0.f;
+                }
+            };
+            int n = 0, items = 0;
+            bool go = wk.begin(a, p);
+            if (go)
+                fetch();
+            while (go) {
+#pragma unroll
+                for (int e = 0; e < TT; ++e)
+                    g[e] = __half_as_ushort(__float2half_rn(raw[e] * fg));
+                const Walk<MODE> me = wk;
+                const bool closes = wk.last();
+                go = wk.next(a, p);
+                if (go)
+                    fetch();
+                if (!warp_mbar_wait_short(&sm->s_full[i], n & 1, abort_flag, a.err))
+                    break;
+                tc_fence_after();
+                uint32_t x[2][16];
+                tmem_ld16(ts, x[0]);
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    const uint32_t(&v)[16] = x[(c / 16) & 1];
+                    tmem_ld_wait();
+                    if (c + 16 < 128)
+                        tmem_ld16(ts + c + 16, x[(c / 16 + 1) & 1]);
+                    uint32_t m[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // (1 or 0, 1 or 0) times the token's 16 bits
+                        const uint32_t on = (uint32_t)__vimin_s32_relu((int)v[2 * e], 1) +
+                                            ((uint32_t)__vimin_s32_relu((int)v[2 * e + 1], 1) << 16);
+                        m[e] = on * g[(c + 2 * e) / HP];
+                    }
+                    tmem_st8(ts + c / 2, m);            // these columns have been read
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->m_full[i]);
+                ++n;
+                if (closes) {
+                    if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
+                        break;
+                    ++items;
+                    tc_fence_after();
+                    // segment of pair `pair` in this CTA's share: both count up, their sum names it
+                    float *o = p.part + ((int64_t)(blockIdx.x + me.pair) * 256 + i * 128 + r) * D;
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(ta + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(o + c + e) =
+                                make_float4(__uint_as_float(v[e]) * inv * inv_w, __uint_as_float(v[e + 1]) * inv * inv_w,
+                                            __uint_as_float(v[e + 2]) * inv * inv_w,
+                                            __uint_as_float(v[e + 3]) * inv * inv_w);
+                    }
+                    tc_fence_before();
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0)
-        a.dw[rh] = (part[0] + part[1] + part[2] + part[3]) * a.q_scale[rh];
-    if ((int)threadIdx.x < a.D)
-        reinterpret_cast<__nv_bfloat16 *>(a.dq)[rh * a.D + threadIdx.x] = __float2bfloat16_rn(acc * a.w[rh]);
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
-// One block per key: thread d owns dk[d]; 128 (token, head) rows at a time.
-__global__ void __launch_bounds__(128) bwd_k_kernel(const ScoresBwdArgs a, const float *G)
+// dk: the partial sums of a pair's segments, added in the order of the shares
+// that made them. Thread = 4 values.
+__global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p, int shares)
 {
-    __shared__ float m[128];
-    const int b = blockIdx.x / a.P;
-    const int j = blockIdx.x - b * a.P;
-    const int8_t *k = a.k8 + (int64_t)blockIdx.x * a.D;
-    const int64_t r0 = (int64_t)b * a.S * a.H;
-    float acc = 0.f;
-    for (int i0 = 0; i0 < a.S * a.H; i0 += 128) {
-        const int i = i0 + threadIdx.x;
-        float v = 0.f;
-        if (i < a.S * a.H) {
-            const float g = G[((int64_t)b * a.S + i / a.H) * a.P + j];
-            if (g != 0.f && dot_codes(a.q8 + (r0 + i) * a.D, k, a.D) > 0)
-                v = g * (a.w[r0 + i] * a.q_scale[r0 + i]);
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per_row = a.D / 4;
+    const int64_t row = id / per_row;
+    if (row >= (int64_t)a.B * a.P)
+        return;
+    const int c = (int)(id - row * per_row) * 4;
+    const int b = (int)(row / a.P), j = (int)(row - (int64_t)b * a.P);
+    const int kp = j >> 8, pair = b * p.n_pairs + kp;
+    long long begin = p.total / a.B * b;
+    for (int k = 0; k < kp; ++k)
+        begin += p.n_steps_seq - first_step(a, p, k);
+    const long long end = begin + p.n_steps_seq - first_step(a, p, kp);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (begin < end) {
+        // share x holds steps [total x / shares, total (x + 1) / shares)
+        int x = (int)((begin * shares) / p.total);
+        while (x > 0 && p.total * x / shares > begin)
+            --x;
+        while (p.total * (x + 1) / shares <= begin)
+            ++x;
+        for (; x < shares && p.total * x / shares < end; ++x) {
+            if (p.total * (x + 1) / shares <= p.total * x / shares)
+                continue;
+            const float4 v = *reinterpret_cast<const float4 *>(p.part + ((int64_t)(x + pair) * 256 + (j & 255)) * a.D + c);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
         }
-        m[threadIdx.x] = v;
-        if (!__syncthreads_or(v != 0.f))
-            continue;
-        if ((int)threadIdx.x < a.D)
-            for (int e = 0; e < min(128, a.S * a.H - i0); ++e)
-                if (m[e] != 0.f)
-                    acc += m[e] * (float)a.q8[(r0 + i0 + e) * a.D + threadIdx.x];
-        __syncthreads();
     }
-    if ((int)threadIdx.x < a.D)
-        reinterpret_cast<__nv_bfloat16 *>(a.dk)[(int64_t)blockIdx.x * a.D + threadIdx.x] = __float2bfloat16_rn(acc);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2 *>(a.dk + row * a.D + c) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
+
+template <int D, int HP>
+cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
+                    cudaStream_t st)
+{
+    CUtensorMap rows, keys;    // query rows (HP heads of TT tokens) and keys, 128 rows a box
+    if (!make_map_q8(&rows, a.q8, D, a.H, (uint64_t)a.B * a.S, HP, 128 / HP) ||
+        !make_map_q8(&keys, a.k8, D, a.P, a.B, 128, 1))
+        return cudaErrorUnknown;
+    cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel<0, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)bw_smem_bytes<D>(true));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(bwd_tc_kernel<1, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)bw_smem_bytes<D>(false));
+    if (e != cudaSuccess)
+        return e;
+    bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true), st>>>(rows, keys, a, pq);
+    if (pk.total > 0)
+        bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false), st>>>(keys, rows, a, pk);
+    const int64_t quads = (int64_t)a.B * a.P * (D / 4);
+    bwd_reduce_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(a, pk, grid_k);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_bwd_heads(int hp, const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
+                          cudaStream_t st)
+{
+    switch (hp) {
+    case 8: return run_bwd<D, 8>(a, pq, pk, grid_q, grid_k, st);
+    case 16: return run_bwd<D, 16>(a, pq, pk, grid_q, grid_k, st);
+    case 32: return run_bwd<D, 32>(a, pq, pk, grid_q, grid_k, st);
+    case 64: return run_bwd<D, 64>(a, pq, pk, grid_q, grid_k, st);
+    default: return run_bwd<D, 128>(a, pq, pk, grid_q, grid_k, st);
+    }
+}
+
+// CTAs of the dk kernel: no more than there are steps if every pair saw every
+// token tile.
+int dk_shares(int B, int S, int H, int P)
+{
+    const int tt = 128 / padded_heads(H);
+    const long long most = (long long)B * ((P + 255) / 256) * ((S + tt - 1) / tt);
+    const int sms = sm_count();
+    return (int)(most < sms ? most : sms);
 }
 
 }  // namespace
 
+// Workspace: the largest magnitudes, a word a token, dk's partial sums, and G.
 size_t indexer_scores_bwd_ws_bytes(int B, int S, int H, int D, int P)
 {
-    (void)H;
-    (void)D;
-    return (size_t)B * S * P * 4;
+    const size_t slots = (size_t)dk_shares(B, S, H, P) + (size_t)B * ((P + 255) / 256);
+    return kMaxWords * 4 + up16((size_t)B * S * 4) + slots * 256 * D * 4 + (size_t)B * S * P * 4;
 }
 
 cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStream_t stream)
 {
-    float *G = static_cast<float *>(ws);
-    bwd_scatter_kernel<<<a.B * a.S, 256, 0, stream>>>(a, G);
-    bwd_q_kernel<<<a.B * a.S * a.H, 128, 0, stream>>>(a, G);
-    bwd_k_kernel<<<a.B * a.P, 128, 0, stream>>>(a, G);
-    return cudaGetLastError();
+    const int sms = sm_count();
+    if (sms <= 0)
+        return cudaErrorUnknown;
+    const int hp = padded_heads(a.H);
+    const int tt = 128 / hp;
+    const int shares = dk_shares(a.B, a.S, a.H, a.P);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    uint32_t *gmax = reinterpret_cast<uint32_t *>(w);
+    uint32_t *row_any = reinterpret_cast<uint32_t *>(w + kMaxWords * 4);
+    float *part = reinterpret_cast<float *>(w + kMaxWords * 4 + up16((size_t)a.B * a.S * 4));
+    BwPlan pk;
+    pk.tt = tt;
+    pk.n_steps_seq = (a.S + tt - 1) / tt;
+    pk.n_pairs = (a.P + 255) / 256;
+    float *G = part + ((size_t)shares + (size_t)a.B * pk.n_pairs) * 256 * a.D;
+    pk.G = a.idx ? G : a.dscores;
+    pk.max = gmax;
+    pk.row = row_any;
+    pk.part = part;
+    long long per_seq = 0;
+    for (int kp = 0; kp < pk.n_pairs; ++kp) {
+        const long long t = (256LL * kp + 1) * a.cr - 1 - a.t_begin;
+        const long long f = t <= 0 ? 0 : t / tt;
+        per_seq += pk.n_steps_seq - (f < pk.n_steps_seq ? f : pk.n_steps_seq);
+    }
+    pk.total = per_seq * a.B;
+    BwPlan pq = pk;
+    pq.n_pairs = (a.S + 2 * tt - 1) / (2 * tt);
+    pq.total = 0;
+    const long long items = (long long)a.B * pq.n_pairs;
+    const int grid_q = (int)(items < sms ? items : sms);
+    cudaError_t e = cudaMemsetAsync(gmax, 0, kMaxWords * 4, stream);
+    if (e != cudaSuccess)
+        return e;
+    bwd_prep_kernel<<<a.B * a.S, kPrepThreads, 0, stream>>>(a, G, gmax, row_any);
+    if (a.D == 32)
+        return run_bwd_heads<32>(hp, a, pq, pk, grid_q, shares, stream);
+    if (a.D == 64)
+        return run_bwd_heads<64>(hp, a, pq, pk, grid_q, shares, stream);
+    return run_bwd_heads<128>(hp, a, pq, pk, grid_q, shares, stream);
 }
 
 }  // namespace sai

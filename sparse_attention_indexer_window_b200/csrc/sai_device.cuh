@@ -307,6 +307,45 @@ __device__ __forceinline__ uint64_t sdesc_k_rows(uint32_t saddr)
     return d;
 }
 
+// D[tmem] (+)= A[tmem] * B[smem desc], fp16 inputs, fp32 accumulate. A row of A
+// is a lane, two consecutive K values a 32-bit column.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: kind::f16 with fp16 A/B, fp32 D, A K-major, B
+// MN-major (its rows run along K).
+__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N)
+{
+    return (1u << 4)                               // D format: f32; A and B format 0: f16
+           | (1u << 16)                            // B is MN-major
+           | ((uint32_t)(N >> 3) << 17)            // N / 8
+           | ((uint32_t)(M >> 4) << 24);           // M / 16
+}
+
+// Shared-memory matrix descriptor for an MN-major operand of 16-bit values:
+// blocks of N_BYTES (its swizzle span: 64 or 128 bytes) of N side by side,
+// block_bytes apart, each with one row per K index, packed in 8-row atoms.
+template <int N_BYTES>
+__device__ __forceinline__ uint64_t sdesc_mn_rows(uint32_t saddr, uint32_t block_bytes)
+{
+    constexpr uint64_t layout = N_BYTES == 128 ? 2 : 4;
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);          // start address
+    d |= (uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16;   // leading byte offset: the next block of N
+    d |= (uint64_t)((8 * N_BYTES) >> 4) << 32;         // stride byte offset: 8 rows of K
+    d |= (uint64_t)1 << 46;                            // descriptor version (sm_100)
+    d |= layout << 61;
+    return d;
+}
+
 // 3-D tiled load of the map's box at element coordinates (x, y, z) into smem.
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x,
                                             int32_t y, int32_t z)

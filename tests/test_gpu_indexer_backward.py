@@ -5,7 +5,9 @@ Tolerances, A being the sum of the terms' magnitudes (tests/q8_ref.py):
   dq, dk  each term may be held in fp16 (2^-11 relative, and an absolute part
           below 2^-36 of the largest term: scaled so that the largest uses the
           type's range), products of scales are rounded in fp32 (a few 2^-24),
-          n terms added in fp32 (n * 2^-24), one rounding to bf16 (2^-8)
+          n terms added in fp32 (n * 2^-24), one rounding to bf16 (2^-8). In dk
+          both factors of a term are held in fp16, G and w q_scale q8: twice
+          2^-11, and 2^-21 for the scale's own 22 bits
   dw      n terms in fp32 and three roundings of products: (n + 4) * 2^-24 * A
 Below fp32's normal range (2^-126) a product G * k_scale, or G * w * q_scale, is
 rounded to a multiple of 2^-149: off by up to 2^-150 however small it is. Each
@@ -66,7 +68,8 @@ def check(got, G, q8, qs, w, k8, ks):
     for name, g, x, a, n, tiny in (("dq", got[0], want[0], mag[0], P, top_k * np.abs(w).max() * P),
                                    ("dk", got[1], want[1], mag[1], S * H, top_q * S * H)):
         g = g.cpu().double().numpy()
-        tol = (2.0 ** -11 + (n + 4) * 2.0 ** -24) * a + 2.0 ** -8 * np.abs(x) + 2.0 ** -36 * 127 * tiny
+        held = 2.0 ** -11 if name == "dq" else 2.0 ** -10 + 2.0 ** -21
+        tol = (held + (n + 4) * 2.0 ** -24) * a + 2.0 ** -8 * np.abs(x) + 2.0 ** -36 * 127 * tiny
         tol = tol + 2.0 ** -150 * 127 * n * (np.abs(w).max() if name == "dq" else 1 + np.abs(G).max()) + 2.0 ** -134
         # (the rounding to bf16 is of the computed value: 2^-8 of the error before it, too)
         d = np.abs(g - x)
@@ -295,3 +298,45 @@ def test_the_whole_step(sai):
                              w[:, pos:pos + 1].contiguous(), cache, scl, cr, block_table=table,
                              q_start=torch.full((1,), pos, dtype=torch.int32, device="cuda"))
     assert torch.equal(one[:, 0], s[:, pos])
+
+
+def test_padding_without_gradient_may_hold_anything(sai):
+    """Tokens that select nothing: their weights and scales (NaN, huge) change
+    nothing, and their own gradients are zero."""
+    B, S, H, D, cr = 2, 150, 16, 64, 2
+    P = S // cr
+    q8, qs, w, k8, ks = inputs(16, B, S, H, D, P)
+    idx, ds = selection(16, ref.candidates(B, S, P, cr), 20)
+    idx[:, 100:] = -1
+    idx[:, 40] = -1
+    want = sai.indexer_scores_backward(*dev(ds, idx, q8, qs, w, k8, ks), cr)
+    w[:, 100:], w[:, 40], qs[:, 120:] = np.nan, 1e30, np.inf
+    got = sai.indexer_scores_backward(*dev(ds, idx, q8, qs, w, k8, ks), cr)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert int((got[0][:, 100:] != 0).sum()) == 0 and int((got[2][:, 40] != 0).sum()) == 0
+
+
+def test_many_slots_of_one_block(sai):
+    """A block named by 300 slots of a token, over more blocks than are gathered at once."""
+    B, S, H, D, cr, P, K = 1, 40, 8, 32, 1, 9000, 300
+    q8, qs, w, k8, ks = inputs(17, B, S, H, D, P)
+    r = np.random.default_rng(17)
+    idx = r.integers(0, P, (B, S, K)).astype(np.int32)
+    idx[:, 3] = 5000
+    idx[:, 9, ::3] = 4096
+    ds = r.standard_normal((B, S, K)).astype(np.float32)
+    mask = np.ones((B, S, P), bool)
+    a = dev(ds, idx, q8, qs, w, k8, ks)
+    got = sai.indexer_scores_backward(*a, cr, t_begin=20000)
+    # G itself is a sum of up to 300 fp32 terms: its rounding is a part of every term's size
+    G = ref.dense(ds, idx, mask)
+    G32 = np.zeros((B, S, P), np.float32)
+    for t in range(S):
+        for k in range(K):
+            G32[0, t, idx[0, t, k]] += ds[0, t, k]
+    assert np.abs(G32 - G).max() < 1e-3
+    check(got, G32.astype(np.float64), q8, qs, w, k8, ks)
+    again = sai.indexer_scores_backward(*a, cr, t_begin=20000)
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)
