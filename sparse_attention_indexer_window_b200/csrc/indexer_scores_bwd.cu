@@ -60,10 +60,11 @@ constexpr int kPrepCols = 4096;         // columns of G gathered at once
 enum { kMaxGk = 0, kMaxG = 1, kMaxW = 2, kMaxWords = 4 };
 
 struct BwPlan {
-    int tt;                // tokens a 128-row tile
+    int tt_log;            // tokens a 128-row tile, as a power of two
     int n_steps_seq;       // dk: token tiles a sequence
     int n_pairs;           // dk: 256-key pairs a sequence; dq: token pairs (2 tt tokens) a sequence
-    long long total;       // dk: steps of the whole batch
+    int per_seq;           // dk: steps of one sequence
+    int share, rest;       // dk: steps of a CTA; the first `rest` CTAs take one more
     const float *G;        // [B,S,P]
     const uint32_t *max;   // kMaxWords
     const uint32_t *row;   // [B,S] not 0 where the token has a gradient
@@ -81,85 +82,78 @@ __device__ __forceinline__ float range_scale(uint32_t bits, int top)
     return ldexpf(1.f, max(-120, min(120, top - e)));
 }
 
-// Candidates [lo, hi) of the token at local index t.
+// Candidates [lo, hi) of the token at local index t (its position fits 31 bits:
+// checked on the host).
 __device__ __forceinline__ void token_range(const ScoresBwdArgs &a, int b, int t, int &lo, int &hi)
 {
-    const int64_t pos = (int64_t)a.t_begin + t;
-    int64_t d0 = a.doc_start ? (int64_t)__ldg(a.doc_start + (int64_t)b * a.S + t) : 0;
-    d0 = d0 < 0 ? 0 : (d0 > pos ? pos : d0);
-    hi = (int)min((int64_t)a.P, (pos + 1) / a.cr);
-    lo = (int)min((int64_t)hi, (d0 + a.cr - 1) / a.cr);
-}
-
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *buf)
-{
-    v = __reduce_max_sync(0xffffffffu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = buf[threadIdx.x & (kPrepThreads / 32 - 1)];
-    return __reduce_max_sync(0xffffffffu, v);
+    const uint32_t pos = (uint32_t)a.t_begin + (uint32_t)t;
+    hi = (int)min((uint32_t)a.P, (pos + 1u) / (uint32_t)a.cr);
+    lo = 0;
+    if (a.doc_start) {
+        const int d = __ldg(a.doc_start + (int64_t)b * a.S + t);
+        const uint32_t d0 = d < 0 ? 0u : min((uint32_t)d, pos);
+        lo = (int)min((uint32_t)hi, (d0 + (uint32_t)a.cr - 1u) / (uint32_t)a.cr);
+    }
 }
 
 // One block a token. With idx: the token's G, gathered in shared memory
-// kPrepCols columns at a time and written out where it has candidates.
-// Slots of one block: two are added in either order to the same bits; a third
-// one (a counter a block notices it) has the columns gathered again by one
-// thread a block in slot order.
+// kPrepCols columns at a time and written out where it has candidates. A
+// block named by one slot (the selection's case) is a plain store, claimed by a
+// bit; if any block is claimed twice, the columns are gathered again by one
+// thread a block in slot order, so that the sum does not depend on timing.
 __global__ void __launch_bounds__(kPrepThreads)
     bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any)
 {
     __shared__ float g[kPrepCols];
-    __shared__ uint32_t cnt[kPrepCols / 4];
-    __shared__ uint32_t buf[kPrepThreads / 32];
+    __shared__ uint32_t claimed[kPrepCols / 32];
+    __shared__ uint32_t buf[4][kPrepThreads / 32];
     const int64_t row = blockIdx.x;
     const int b = (int)(row / a.S);
     const int t = (int)(row - (int64_t)b * a.S);
     int lo, hi;
     token_range(a, b, t, lo, hi);
-    uint32_t any = 0, top_g = 0, top_gk = 0;
-    // the largest finite magnitude: one NaN or infinity does not unscale the others
+    // the largest finite magnitudes: one NaN or infinity does not unscale the others
     auto finite = [](float v) {
         const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
         return u < 0x7f800000u ? u : 0u;
     };
+    uint32_t top[4] = {0u, 0u, 0u, 0u};              // kMaxGk, kMaxG, kMaxW; any gradient at all
     const float *ks = a.k_scale + (int64_t)b * a.P;
     const float *ds = a.dscores + row * a.K;
     auto seen = [&](float v, int j) {
         if (v != 0.f) {
-            any = 1u;
-            top_g = max(top_g, finite(v));
-            top_gk = max(top_gk, finite(v * __ldg(ks + j)));
+            top[3] = 1u;
+            top[kMaxG] = max(top[kMaxG], finite(v));
+            top[kMaxGk] = max(top[kMaxGk], finite(v * __ldg(ks + j)));
         }
     };
+    for (int h = threadIdx.x; h < a.H; h += kPrepThreads)
+        top[kMaxW] = max(top[kMaxW], finite(__ldg(a.w + row * a.H + h) * __ldg(a.q_scale + row * a.H + h)));
     if (!a.idx) {
         for (int j = lo + threadIdx.x; j < hi; j += kPrepThreads)
             seen(__ldg(ds + j), j);
     } else {
         const int32_t *idx = a.idx + row * a.K;
-        for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
-            const int j = __ldg(idx + k);
-            if ((j < -1 || j >= a.P) && a.err)
-                atomicExch(a.err, kErrIndex);
-        }
-        for (int c0 = lo / 4 * 4; c0 < hi; c0 += kPrepCols) {
-            const int n = min(kPrepCols, hi - c0);
+        for (int c0 = lo & ~31; c0 < hi || c0 == (lo & ~31); c0 += kPrepCols) {
+            const int n = max(0, min(kPrepCols, hi - c0));
             for (int j = threadIdx.x; j < n; j += kPrepThreads)
                 g[j] = 0.f;
-            for (int j = threadIdx.x; j < (n + 3) / 4; j += kPrepThreads)
-                cnt[j] = 0u;
+            for (int j = threadIdx.x; j < (n + 31) / 32; j += kPrepThreads)
+                claimed[j] = 0u;
             __syncthreads();
-            bool third = false;
+            bool twice = false;
             for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
                 const int id = __ldg(idx + k), j = id - c0;
+                if ((id < -1 || id >= a.P) && a.err)
+                    atomicExch(a.err, kErrIndex);
                 if (id < lo || id >= hi || j < 0 || j >= n)
                     continue;
-                atomicAdd(&g[j], __ldg(ds + k));
-                const uint32_t old = atomicAdd(&cnt[j >> 2], 1u << (8 * (j & 3)));
-                third |= ((old >> (8 * (j & 3))) & 255u) >= 2u;
+                if (atomicOr(&claimed[j >> 5], 1u << (j & 31)) & (1u << (j & 31)))
+                    twice = true;
+                else
+                    g[j] = __ldg(ds + k);
             }
-            if (__syncthreads_or(third)) {
+            if (__syncthreads_or(twice)) {
                 for (int j = threadIdx.x; j < n; j += kPrepThreads)
                     g[j] = 0.f;
                 __syncthreads();
@@ -179,26 +173,32 @@ __global__ void __launch_bounds__(kPrepThreads)
             __syncthreads();
         }
     }
-    any = block_max(any, buf);
-    if (threadIdx.x == 0)
-        row_any[row] = any;
-    if (any == 0u)
-        return;
-    top_g = block_max(top_g, buf);
-    top_gk = block_max(top_gk, buf);
-    uint32_t top_w = 0;
-    for (int h = threadIdx.x; h < a.H; h += kPrepThreads)
-        top_w = max(top_w, finite(a.w[row * a.H + h] * a.q_scale[row * a.H + h]));
-    top_w = block_max(top_w, buf);
-    if (threadIdx.x < 3) {
-        const uint32_t v = threadIdx.x == kMaxGk ? top_gk : (threadIdx.x == kMaxG ? top_g : top_w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        top[e] = __reduce_max_sync(0xffffffffu, top[e]);
+        if ((threadIdx.x & 31) == 0)
+            buf[e][threadIdx.x >> 5] = top[e];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+        uint32_t v = 0, any = 0;
+#pragma unroll
+        for (int i = 0; i < kPrepThreads / 32; ++i) {
+            v = max(v, buf[threadIdx.x][i]);
+            any |= buf[3][i];
+        }
+        if (threadIdx.x == 3)
+            row_any[row] = any;
         // (a stale word only means one more atomic)
-        if (v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
+        else if (any && v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
             atomicMax(gmax + threadIdx.x, v);
     }
 }
 
 // ------------------------------------------------------------ the walk
+// dk: first step of CTA x's share of the batch's steps.
+__device__ __forceinline__ int share_start(const BwPlan &p, int x) { return x * p.share + min(x, p.rest); }
+
 // The steps of one CTA, the same for every role: dq walks items blockIdx.x,
 // + gridDim.x, ... (2 tt tokens each, late tokens first) and their key tiles;
 // dk walks a contiguous share of all steps of the batch (a pair of key tiles
@@ -211,14 +211,14 @@ struct Walk {
     int pair;           // dk: pair of the batch
     // position
     int item;
-    long long at, end;
+    int at, end;
 
     __device__ __forceinline__ bool set(const ScoresBwdArgs &a, const BwPlan &p);
     __device__ __forceinline__ bool begin(const ScoresBwdArgs &a, const BwPlan &p)
     {
         item = (int)blockIdx.x;
-        at = p.total * blockIdx.x / gridDim.x;
-        end = p.total * (blockIdx.x + 1) / gridDim.x;
+        at = share_start(p, (int)blockIdx.x);
+        end = share_start(p, (int)blockIdx.x + 1);
         return set(a, p);
     }
     __device__ __forceinline__ bool next(const ScoresBwdArgs &a, const BwPlan &p)
@@ -237,7 +237,7 @@ struct Walk {
 __device__ __forceinline__ int first_step(const ScoresBwdArgs &a, const BwPlan &p, int kp)
 {
     const int64_t t = (int64_t)(256 * (int64_t)kp + 1) * a.cr - 1 - a.t_begin;
-    return t <= 0 ? 0 : (int)min((int64_t)p.n_steps_seq, t / p.tt);
+    return t <= 0 ? 0 : (int)min((int64_t)p.n_steps_seq, t >> p.tt_log);
 }
 
 template <>
@@ -245,10 +245,10 @@ __device__ __forceinline__ bool Walk<0>::set(const ScoresBwdArgs &a, const BwPla
 {
     for (; item < a.B * p.n_pairs; item += gridDim.x) {
         b = item % a.B;
-        a0 = (p.n_pairs - 1 - item / a.B) * 2 * p.tt;
-        const int64_t t_last = min(a.S, a0 + 2 * p.tt) - 1;
+        a0 = (p.n_pairs - 1 - item / a.B) << (p.tt_log + 1);
+        const uint32_t seen = (uint32_t)a.t_begin + (uint32_t)min(a.S, a0 + (2 << p.tt_log));
         s = 0;
-        s_end = (int)((min((int64_t)a.P, ((int64_t)a.t_begin + t_last + 1) / a.cr) + 127) / 128);
+        s_end = (int)((min((uint32_t)a.P, seen / (uint32_t)a.cr) + 127u) / 128u);
         first = true;
         if (s_end > 0)
             return true;
@@ -262,17 +262,16 @@ __device__ __forceinline__ bool Walk<1>::set(const ScoresBwdArgs &a, const BwPla
 {
     if (at >= end)
         return false;
-    const long long per_seq = p.total / a.B;
-    b = (int)(at / per_seq);
-    long long r = at - b * per_seq;
+    b = at / p.per_seq;
+    int r = at - b * p.per_seq;
     int kp = 0, f = first_step(a, p, 0);
     while (r >= p.n_steps_seq - f) {
         r -= p.n_steps_seq - f;
         f = first_step(a, p, ++kp);
     }
-    s = f + (int)r;
-    const long long n = min((long long)(p.n_steps_seq - s), end - at);
-    s_end = s + (int)n;
+    s = f + r;
+    const int n = min(p.n_steps_seq - s, end - at);
+    s_end = s + n;
     at += n;
     a0 = kp * 256;
     pair = b * p.n_pairs + kp;
@@ -283,20 +282,20 @@ __device__ __forceinline__ bool Walk<1>::set(const ScoresBwdArgs &a, const BwPla
 struct BwSmem {
     uint64_t a_full[2], a_empty[2];
     uint64_t b_full[kBwRing], b_empty[kBwRing];
-    uint64_t c_full[2], c_empty[2];      // fp16 tiles
-    uint64_t s_full[2], m_full[2];       // per stationary tile: products there; M there
+    uint64_t c_empty[2];                 // fp16 tiles
+    uint64_t s_full[2];                  // per stationary tile: products there
+    uint64_t m_full[3];                  // M there; of the first tile B2 too (even steps, odd steps), of the second
     uint64_t acc_full[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    int lo[2][kBwMaxTok], hi[2][kBwMaxTok];        // dq: the tokens' candidates, per tile
 };
 
 template <int D>
 constexpr size_t bw_smem_bytes(bool dq)
 {
     return 1024 + 4 * 128 * D + (size_t)kBwRing * 128 * D + 2 * 128 * D * 2 +
-           (dq ? 2 * 2 * (size_t)kBwMaxTok * kBwRow * 4 : 0) + sizeof(BwSmem);
+           (dq ? 2 * 2 * (size_t)kBwMaxTok * kBwRow * 4 + 8 * 2048 : 0) + sizeof(BwSmem);
 }
 
 // Offset of 16-byte chunk c of row r in a tile of ROW_BYTES rows stored with
@@ -327,9 +326,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     uint8_t *sa = base;                                // [2 items][2 tiles]
     uint8_t *sb = sa + 4 * tile8;                      // [ring]
     uint8_t *sc = sb + kBwRing * tile8;                // [2] fp16
-    float *sg = reinterpret_cast<float *>(sc + 2 * tile16);   // dq: [2 tiles][2][kBwMaxTok][kBwRow] gk
+    float *sg = reinterpret_cast<float *>(sc + 2 * tile16);   // dq: [2 tiles][2][kBwMaxTok][kBwRow] gk,
+                                                              // then 2 KB of output a warp
     BwSmem *sm = reinterpret_cast<BwSmem *>(reinterpret_cast<uint8_t *>(sg) +
-                                            (MODE == 0 ? 4 * kBwMaxTok * kBwRow * 4 : 0));
+                                            (MODE == 0 ? 4 * kBwMaxTok * kBwRow * 4 + 8 * 2048 : 0));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -337,16 +337,16 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->a_full[i], 1);
             mbar_init(&sm->a_empty[i], 1);
-            mbar_init(&sm->c_full[i], 4);
             mbar_init(&sm->c_empty[i], 1);
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->m_full[i], 4);
+            mbar_init(&sm->m_full[i], 4 + 4);       // the epilogue's warps and the converters, who run a step ahead
             mbar_init(&sm->acc_full[i], 1);
         }
         for (int i = 0; i < kBwRing; ++i) {
             mbar_init(&sm->b_full[i], 1);
-            mbar_init(&sm->b_empty[i], 1 + 4);
+            mbar_init(&sm->b_empty[i], 1 + 4);      // products done (passed on by a warp); converted
         }
+        mbar_init(&sm->m_full[2], 4);
         mbar_init(&sm->drain, 1);
         sm->abort_flag = 0;
         fence_mbar_init();
@@ -425,92 +425,84 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        constexpr uint32_t id_s = idesc_i8_s32(128, 128);
-        constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
-        int stage = 0, item = -1, n = 0;
-        uint32_t phase = 0;
-        bool ok = true, issued = false;
-        auto products = [&](int i) {
-            // S_i = A_i B^T of the walk's step (lane 0)
-            const uint64_t da = sdesc_k_rows<D>(smem_u32(sa + (2 * (item & 1) + i) * tile8));
-            const uint64_t db = sdesc_k_rows<D>(smem_u32(sb + stage * tile8));
+        // One thread runs this role alone: a wait or a commit costs it about 150
+        // cycles, so it has three waits and two commits a step; everything else
+        // that must be known done (code tiles read, fp16 tiles read) follows from
+        // the second tile's products of the next step and is passed on by the
+        // warps that wait for those.
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_i8_s32(128, 128);
+            constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
+            int stage = 0, item = -1, n = 0;
+            uint32_t phase = 0;
+            bool issued = false;
+            auto products = [&](int i) {
+                // S_i = A_i B^T of the walk's step
+                const uint64_t da = sdesc_k_rows<D>(smem_u32(sa + (2 * (item & 1) + i) * tile8));
+                const uint64_t db = sdesc_k_rows<D>(smem_u32(sb + stage * tile8));
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-                umma_i8(tmem + i * 128, da + 2 * kk, db + 2 * kk, id_s, kk != 0);
-            umma_commit(&sm->s_full[i]);
-        };
-        // the step whose tiles are in place next
-        auto arrive_step = [&]() -> bool {
-            if (wk.first) {
-                ++item;
-                if (!warp_mbar_wait_short(&sm->a_full[item & 1], (item >> 1) & 1, abort_flag, a.err))
-                    return false;
-            }
-            return warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err);
-        };
-        auto done_step = [&]() {
-            // after both tiles' products of the step are issued
-            if (lane == 0) {
-                umma_commit(&sm->b_empty[stage]);
+                for (int kk = 0; kk < D / 32; ++kk)
+                    umma_i8(tmem + i * 128, da + 2 * kk, db + 2 * kk, id_s, kk != 0);
+                umma_commit(&sm->s_full[i]);
+            };
+            // the walk's step: its tiles are in place
+            auto arrive_step = [&]() -> bool {
+                if (wk.first) {
+                    ++item;
+                    if (!mbar_wait_short(&sm->a_full[item & 1], (item >> 1) & 1, abort_flag, a.err))
+                        return false;
+                }
+                return mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err);
+            };
+            auto done_step = [&]() {
                 if (wk.last())
                     umma_commit(&sm->a_empty[item & 1]);
-            }
-            __syncwarp();
-            if (++stage == kBwRing) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        };
-        bool go = wk.begin(a, p);
-        if (go) {
-            ok = arrive_step();
-            if (ok) {
-                tc_fence_after();
-                if (lane == 0) {
+                if (++stage == kBwRing) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
+            bool go = wk.begin(a, p), ok = true;
+            if (go) {
+                ok = arrive_step();
+                if (ok) {
+                    tc_fence_after();
                     products(0);
                     products(1);
                     issued = true;
+                    done_step();
                 }
-                __syncwarp();
-                done_step();
             }
-        }
-        while (go && ok) {
-            const bool fresh = wk.first, closes = wk.last();
-            const int cb = n & 1;
-            const uint64_t dc = sdesc_mn_rows<kC>(smem_u32(sc + cb * tile16), 128 * kC);
-            go = wk.next(a, p);                  // the walk is now one step ahead
-            for (int i = 0; i < 2 && ok; ++i) {
-                ok = warp_mbar_wait_short(&sm->m_full[i], n & 1, abort_flag, a.err);
-                if (ok && i == 0) {
-                    ok = warp_mbar_wait_short(&sm->c_full[cb], (n >> 1) & 1, abort_flag, a.err);
-                    if (ok && go)
-                        ok = arrive_step();
-                }
-                if (!ok)
+            while (go && ok) {
+                const bool fresh = wk.first, closes = wk.last();
+                const uint64_t dc = sdesc_mn_rows<kC>(smem_u32(sc + (n & 1) * tile16), 128 * kC);
+                go = wk.next(a, p);                  // the walk is now one step ahead
+                if (go && !arrive_step())
                     break;
-                tc_fence_after();
-                if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ok = i == 0 ? mbar_wait_short(&sm->m_full[n & 1], (n >> 1) & 1, abort_flag, a.err)
+                                : mbar_wait_short(&sm->m_full[2], n & 1, abort_flag, a.err);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_f16_ta(tmem + 256 + i * D, tmem + i * 128 + kk * 8, dc + kk * (16 * kC / 16), id_acc,
+                        umma_f16_ta(tmem + 256 + i * D, tmem + i * 128 + kk * 8, dc + kk * kC, id_acc,
                                     (kk != 0 || !fresh) ? 1u : 0u);
                     if (closes)
                         umma_commit(&sm->acc_full[i]);
-                    if (i == 1)
-                        umma_commit(&sm->c_empty[cb]);
                     if (go)
                         products(i);
                 }
-                __syncwarp();
+                if (ok && go)
+                    done_step();
+                ++n;
             }
-            if (ok && go)
-                done_step();
-            ++n;
-        }
-        if (!ok && lane == 0 && issued) {
-            umma_commit(&sm->drain);
-            mbar_drain(&sm->drain, 0);
+            if (*abort_flag && issued) {
+                umma_commit(&sm->drain);
+                mbar_drain(&sm->drain, 0);
+            }
         }
         __syncwarp();
     } else if (warp >= 12) {
@@ -574,7 +566,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sm->c_full[cb]);
+                mbar_arrive(&sm->m_full[cb]);
                 mbar_arrive(&sm->b_empty[stage]);
             }
             scale = next_scale;
@@ -590,44 +582,54 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         const int q = warp & 3;
         const int r = q * 32 + lane;                   // tile row
         const uint32_t ts = tmem + i * 128 + ((uint32_t)(q * 32) << 16);
+        // One warp of the second tile passes on what its products of step n imply:
+        // step n's code tile and step n-1's fp16 tile have been read.
+        int ring = 0;
+        auto pass_on = [&](int n) {
+            if (i == 1 && q == 0 && lane == 0) {
+                mbar_arrive(&sm->b_empty[ring]);
+                if (n > 0)
+                    mbar_arrive(&sm->c_empty[(n - 1) & 1]);
+            }
+            if (++ring == kBwRing)
+                ring = 0;
+        };
         const uint32_t ta = tmem + 256 + i * D + ((uint32_t)(q * 32) << 16);
         if constexpr (MODE == 0) {
             const float f = range_scale(__ldg(p.max + kMaxGk), 15);
             const float inv = 1.f / f;
             const int tt = r / HP, h = r % HP;
             float *stage0 = sg + i * 2 * kBwMaxTok * kBwRow;
+            uint4 *out = reinterpret_cast<uint4 *>(sg + 4 * kBwMaxTok * kBwRow) + (warp - 4) * 128;
             // Items without a candidate never reach the walk: their gradients are zero.
             for (int it = (int)blockIdx.x; it < a.B * p.n_pairs; it += gridDim.x) {
-                const int b = it % a.B, t = (p.n_pairs - 1 - it / a.B) * 2 * TT + i * TT + tt;
-                const int64_t t_last = min(a.S, (p.n_pairs - 1 - it / a.B) * 2 * TT + 2 * TT) - 1;
-                if (((int64_t)a.t_begin + t_last + 1) / a.cr > 0 || t >= a.S || h >= a.H)
+                const int b = it % a.B, a0 = (p.n_pairs - 1 - it / a.B) * 2 * TT, t = a0 + i * TT + tt;
+                if (((uint32_t)a.t_begin + (uint32_t)min(a.S, a0 + 2 * TT)) / (uint32_t)a.cr > 0 || t >= a.S || h >= a.H)
                     continue;
                 const int64_t row = ((int64_t)b * a.S + t) * a.H + h;
                 a.dw[row] = 0.f;
                 for (int c = 0; c < D / 8; ++c)
                     reinterpret_cast<uint4 *>(a.dq + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
             }
-            // gk of the step's 128 keys and this tile's tokens: thread = key, one value a token
+            // gk of the step's 128 keys and this tile's tokens: thread = key, one value a token;
+            // lane e holds token e's candidates
             float g[TT], ksv = 0.f;
+            int lo = 0, hi = 0;
+            auto bounds = [&]() {
+                const int t = wk.a0 + i * TT + lane;
+                lo = hi = 0;
+                if (lane < TT && t < a.S)
+                    token_range(a, wk.b, t, lo, hi);
+            };
             auto fetch = [&]() {
                 const int j = wk.s * 128 + r;
                 ksv = j < a.P ? __ldg(a.k_scale + (int64_t)wk.b * a.P + j) : 0.f;
                 const float *src = p.G + ((int64_t)wk.b * a.S + wk.a0 + i * TT) * a.P + j;
 #pragma unroll
-                for (int e = 0; e < TT; ++e)
-                    g[e] = j >= sm->lo[i][e] && j < sm->hi[i][e] ? __ldg(src + (int64_t)e * a.P) : 0.f;
-            };
-            auto bounds = [&]() {
-                named_bar_sync(1 + i, 128);
-                if (r < TT) {
-                    const int t = wk.a0 + i * TT + r;
-                    int lo = 0, hi = 0;
-                    if (t < a.S)
-                        token_range(a, wk.b, t, lo, hi);
-                    sm->lo[i][r] = lo;
-                    sm->hi[i][r] = hi;
+                for (int e = 0; e < TT; ++e) {
+                    const int l = __shfl_sync(0xffffffffu, lo, e), u = __shfl_sync(0xffffffffu, hi, e);
+                    g[e] = j >= l && j < u ? __ldg(src + (int64_t)e * a.P) : 0.f;
                 }
-                named_bar_sync(1 + i, 128);
             };
             auto put = [&](int buf) {
 #pragma unroll
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                     ok = false;
                     continue;
                 }
+                pass_on(n);
                 tc_fence_after();
                 const float *gk = stage0 + ((n & 1) * kBwMaxTok + tt) * kBwRow;
                 uint32_t x[2][16];
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sm->m_full[i]);
+                    mbar_arrive(&sm->m_full[i == 0 ? n & 1 : 2]);
                 ++n;
                 if (closes) {
                     if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err)) {
@@ -709,22 +712,39 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                     if (mine)
                         a.dw[row] = any ? ((dw[0] + dw[1]) + (dw[2] + dw[3])) * inv * __ldg(a.q_scale + row) : 0.f;
                     dw[0] = dw[1] = dw[2] = dw[3] = 0.f;
+                    // 32 values of the warp's 32 rows at a time, through shared memory: four
+                    // lanes store one row's 64 bytes, not 32 lanes 16 bytes of 32 rows
+                    const uint32_t my_row = mine ? (uint32_t)row : 0xffffffffu;     // B S H fits 31 bits
+                    uint32_t dst[4];
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t v[16], o[8];
-                        tmem_ld16(ta + c, v);
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = __shfl_sync(0xffffffffu, my_row, e * 8 + (lane >> 2));
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[2][16];
+                        tmem_ld16(ta + c, v[0]);
+                        tmem_ld16(ta + c + 16, v[1]);
                         tmem_ld_wait();
+                        __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float y0 = any ? __uint_as_float(v[2 * e]) * wq : 0.f;
-                            const float y1 = any ? __uint_as_float(v[2 * e + 1]) * wq : 0.f;
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
-                            o[e] = *reinterpret_cast<const uint32_t *>(&y);
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float y0 = any ? __uint_as_float(v[u / 2][(u % 2) * 8 + 2 * e]) * wq : 0.f;
+                                const float y1 = any ? __uint_as_float(v[u / 2][(u % 2) * 8 + 2 * e + 1]) * wq : 0.f;
+                                const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
+                                o[e] = *reinterpret_cast<const uint32_t *>(&y);
+                            }
+                            out[lane * 4 + (u ^ ((lane >> 1) & 3))] = make_uint4(o[0], o[1], o[2], o[3]);
                         }
-                        if (mine) {
-                            uint4 *d = reinterpret_cast<uint4 *>(a.dq + row * D + c);
-                            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int l = e * 8 + (lane >> 2), u = lane & 3;
+                            const uint4 o = out[l * 4 + (u ^ ((l >> 1) & 3))];
+                            if (dst[e] != 0xffffffffu)
+                                *reinterpret_cast<uint4 *>(a.dq + (int64_t)dst[e] * D + c + u * 8) = o;
                         }
                     }
                     tc_fence_before();
@@ -764,6 +784,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                     fetch();
                 if (!warp_mbar_wait_short(&sm->s_full[i], n & 1, abort_flag, a.err))
                     break;
+                pass_on(n);
                 tc_fence_after();
                 uint32_t x[2][16];
                 tmem_ld16(ts, x[0]);
@@ -787,7 +808,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sm->m_full[i]);
+                    mbar_arrive(&sm->m_full[i == 0 ? n & 1 : 2]);
                 ++n;
                 if (closes) {
                     if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
@@ -823,41 +844,48 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 }
 
 // dk: the partial sums of a pair's segments, added in the order of the shares
-// that made them. Thread = 4 values.
+// that made them. Thread = 4 values; a block stays within one pair's 256 keys.
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p, int shares)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int per_row = a.D / 4;
-    const int64_t row = id / per_row;
-    if (row >= (int64_t)a.B * a.P)
+    const int per_row = a.D / 4, rows = 256 / per_row;       // keys a block
+    const int pair = (int)(blockIdx.x / per_row);            // 256 / rows = per_row blocks a pair
+    const int b = pair / p.n_pairs, kp = pair - b * p.n_pairs;
+    const int in = (int)(blockIdx.x - pair * per_row) * rows + threadIdx.x / per_row;
+    const int c = (threadIdx.x % per_row) * 4;
+    const int j = kp * 256 + in;
+    if (j >= a.P)
         return;
-    const int c = (int)(id - row * per_row) * 4;
-    const int b = (int)(row / a.P), j = (int)(row - (int64_t)b * a.P);
-    const int kp = j >> 8, pair = b * p.n_pairs + kp;
-    long long begin = p.total / a.B * b;
+    int begin = p.per_seq * b;
     for (int k = 0; k < kp; ++k)
         begin += p.n_steps_seq - first_step(a, p, k);
-    const long long end = begin + p.n_steps_seq - first_step(a, p, kp);
+    const int end = begin + p.n_steps_seq - first_step(a, p, kp);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (begin < end) {
-        // share x holds steps [total x / shares, total (x + 1) / shares)
-        int x = (int)((begin * shares) / p.total);
-        while (x > 0 && p.total * x / shares > begin)
-            --x;
-        while (p.total * (x + 1) / shares <= begin)
-            ++x;
-        for (; x < shares && p.total * x / shares < end; ++x) {
-            if (p.total * (x + 1) / shares <= p.total * x / shares)
-                continue;
-            const float4 v = *reinterpret_cast<const float4 *>(p.part + ((int64_t)(x + pair) * 256 + (j & 255)) * a.D + c);
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+        // the share that holds step `begin`
+        const int longer = p.rest * (p.share + 1);
+        int x = begin < longer ? begin / (p.share + 1) : p.rest + (begin - longer) / p.share;
+        const float *src = p.part + ((int64_t)(x + pair) * 256 + in) * a.D + c;
+        int n = 0;
+        while (x + n < shares && share_start(p, x + n) < end)
+            ++n;
+        // eight loads in flight; the sums in the shares' order
+        for (int i = 0; i < n; i += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = i + e < n ? __ldcs(reinterpret_cast<const float4 *>(src + (int64_t)(i + e) * 256 * a.D))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s.x += v[e].x;
+                s.y += v[e].y;
+                s.z += v[e].z;
+                s.w += v[e].w;
+            }
         }
     }
     const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-    *reinterpret_cast<uint2 *>(a.dk + row * a.D + c) =
+    *reinterpret_cast<uint2 *>(a.dk + ((int64_t)b * a.P + j) * a.D + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
@@ -879,10 +907,9 @@ cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, 
     if (e != cudaSuccess)
         return e;
     bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true), st>>>(rows, keys, a, pq);
-    if (pk.total > 0)
+    if (grid_k > 0)
         bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false), st>>>(keys, rows, a, pk);
-    const int64_t quads = (int64_t)a.B * a.P * (D / 4);
-    bwd_reduce_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(a, pk, grid_k);
+    bwd_reduce_kernel<<<(unsigned)(a.B * pk.n_pairs * (D / 4)), 256, 0, st>>>(a, pk, grid_k);
     return cudaGetLastError();
 }
 
@@ -925,13 +952,15 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
         return cudaErrorUnknown;
     const int hp = padded_heads(a.H);
     const int tt = 128 / hp;
-    const int shares = dk_shares(a.B, a.S, a.H, a.P);
+    int shares = dk_shares(a.B, a.S, a.H, a.P);
     uint8_t *w = static_cast<uint8_t *>(ws);
     uint32_t *gmax = reinterpret_cast<uint32_t *>(w);
     uint32_t *row_any = reinterpret_cast<uint32_t *>(w + kMaxWords * 4);
     float *part = reinterpret_cast<float *>(w + kMaxWords * 4 + up16((size_t)a.B * a.S * 4));
     BwPlan pk;
-    pk.tt = tt;
+    pk.tt_log = 0;
+    while ((1 << pk.tt_log) < tt)
+        ++pk.tt_log;
     pk.n_steps_seq = (a.S + tt - 1) / tt;
     pk.n_pairs = (a.P + 255) / 256;
     float *G = part + ((size_t)shares + (size_t)a.B * pk.n_pairs) * 256 * a.D;
@@ -945,10 +974,14 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
         const long long f = t <= 0 ? 0 : t / tt;
         per_seq += pk.n_steps_seq - (f < pk.n_steps_seq ? f : pk.n_steps_seq);
     }
-    pk.total = per_seq * a.B;
+    const long long total = per_seq * a.B;       // fits 31 bits (checked on the host)
+    if (total < shares)
+        shares = (int)total;                     // no empty share
+    pk.per_seq = (int)per_seq;
+    pk.share = shares ? (int)(total / shares) : 0;
+    pk.rest = shares ? (int)(total % shares) : 0;
     BwPlan pq = pk;
     pq.n_pairs = (a.S + 2 * tt - 1) / (2 * tt);
-    pq.total = 0;
     const long long items = (long long)a.B * pq.n_pairs;
     const int grid_q = (int)(items < sms ? items : sms);
     cudaError_t e = cudaMemsetAsync(gmax, 0, kMaxWords * 4, stream);

@@ -149,7 +149,7 @@ sai_status sai_indexer_scores_backward(const float *dscores, const int32_t *idx,
     if (e != SAI_OK)
         return e;
     if (K < 1 || K > P || (!idx && K != P) || t_begin < 0 || (int64_t)t_begin + S > INT32_MAX ||
-        (int64_t)S * H > INT32_MAX / 2)
+        (int64_t)B * ((P + 255LL) / 256) * ((S + 127LL) / 128 * sai::padded_heads(H) + 1) > INT32_MAX)
         return SAI_ERR_SHAPE;
     if (!al4(dscores) || (idx && !al4(idx)) || !al16(q8) || !al4(q_scale) || !al4(w) || !al16(k8) ||
         !al4(k_scale) || !al16(dq) || !al16(dk) || !al4(dw) || (doc_start && !al4(doc_start)) ||

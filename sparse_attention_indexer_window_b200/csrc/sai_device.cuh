@@ -117,34 +117,36 @@ __device__ __forceinline__ bool warp_mbar_wait(uint64_t *bar, uint32_t parity, v
     return __all_sync(0xffffffffu, ok);
 }
 
-// warp_mbar_wait for kernels whose waits are short and many (a tile of a few
+// mbar_wait (one thread's, a warp's) for kernels whose waits are short and many (a tile of a few
 // hundred nanoseconds): the clock, whose read costs as much as such a wait, is
 // read only once a wait has lasted 32 tries. The same limit and outcome.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                                int32_t *err)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !mbar_try_wait_sleep(bar, parity, kWaitSleepNs); ++it) {
+        if ((it & 31u) != 0)
+            continue;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0)
+            t0 = now;
+        if (*abort_flag)
+            return false;
+        if (now - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            if (err)
+                atomicExch(err, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
 __device__ __forceinline__ bool warp_mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                                      int32_t *err)
 {
-    bool ok = true;
-    if (!mbar_try_wait(bar, parity)) {
-        uint64_t t0 = 0;
-        for (uint32_t it = 1; !mbar_try_wait_sleep(bar, parity, kWaitSleepNs); ++it) {
-            if ((it & 31u) != 0)
-                continue;
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0)
-                t0 = now;
-            if (*abort_flag) {
-                ok = false;
-                break;
-            }
-            if (now - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                if (err)
-                    atomicExch(err, kErrTimeout);
-                ok = false;
-                break;
-            }
-        }
-    }
+    const bool ok = mbar_wait_short(bar, parity, abort_flag, err);
     return __all_sync(0xffffffffu, ok);
 }
 
