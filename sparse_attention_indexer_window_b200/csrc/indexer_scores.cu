@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     constexpr uint32_t q_bytes = kScCols * D, k_bytes = 128 * D;
     uint8_t *sq = base, *sk = base + kScItems * q_bytes;
     ScSmem *sm = reinterpret_cast<ScSmem *>(sk + kScRing * k_bytes);
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform_warp();
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         const uint32_t idesc = idesc_i8_s32(128, cols);
+        const uint64_t q_desc = sdesc_k_rows<D>(smem_u32(sq)), k_desc = sdesc_k_rows<D>(smem_u32(sk));
         int stage = 0, slot = 0, n_tiles = 0;
         uint32_t phase = 0, iphase = 0;
         bool ok = true, issued = false;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 break;
             }
             const int n_live = sm->item[slot].k_hi - sm->item[slot].k_lo;
-            const uint64_t db = sdesc_k_rows<D>(smem_u32(sq + slot * q_bytes));
+            const uint64_t db = q_desc + slot * (q_bytes / 16);
             for (int k = 0; k < n_live; ++k, ++n_tiles) {
                 const int buf = n_tiles & ((1 << acc_log) - 1);
                 if (!warp_mbar_wait_short(&sm->acc_empty[buf], ((n_tiles >> acc_log) & 1) ^ 1u, abort_flag, a.err) ||
@@ -270,14 +271,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t da = sdesc_k_rows<D>(smem_u32(sk + stage * k_bytes));
+                const uint64_t da = k_desc + stage * (k_bytes / 16);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk)
                         umma_i8(tmem + buf * acc_cols, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
                     umma_commit(&sm->acc_full[buf]);
-                    issued = true;
                 }
+                issued = true;
                 __syncwarp();
                 if (++stage == kScRing) {
                     stage = 0;

@@ -34,10 +34,14 @@
 //
 // Bound: per 128 x 128 tile of D = 128, 256 cycles of kind::i8 and 512 of
 // kind::f16 on the tensor pipe. The two stationary tiles alternate: while one's
-// M is formed the other's products run. Warp roles (512 threads): warp 0 TMA,
-// warp 1 MMA issue, warps 4..7 and 8..11 the epilogues of the two tiles, warps
-// 12..15 turn B's codes into fp16. Every wait is bounded; on timeout the kernel
-// records SAI_ERR_TIMEOUT and unwinds.
+// M is formed the other's products run. Warp roles: warp 0 TMA, warps 1 and 2
+// issue the MMAs of one tile each (one warp for both left the tensor pipe idle
+// through its waits), warps 4..11 and 12..19 the epilogues of the two tiles (two
+// warps for each 32 lanes, 64 columns each). The halves are four chains of
+// products, M, second products and the next products in the same place, so that
+// some are with the tensor pipe while others form M. Warps 20..27 turn B's codes
+// into fp16 (dq: four of them, the other four stage gk). Every wait is bounded;
+// on timeout the kernel records SAI_ERR_TIMEOUT and unwinds.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -49,10 +53,12 @@
 namespace sai {
 namespace {
 
-constexpr int kBwThreads = 512;
+constexpr int kBwThreads = 896;
 constexpr int kBwRing = 3;              // code tiles B in flight
-constexpr int kBwMaxTok = 16;           // tokens of a 128-row tile (HP = 8)
-constexpr int kBwRow = 132;             // floats between two tokens' staged gk (4 more than a tile: no bank conflicts)
+// Floats between two tokens' staged gk: four more than a tile where a warp's lanes
+// span few tokens, so that they use other banks (with 16 tokens a tile the shared
+// memory has no room for it).
+constexpr int gk_row(int hp) { return hp == 8 ? 128 : 132; }
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCols = 4096;         // columns of G gathered at once
 
@@ -282,21 +288,28 @@ __device__ __forceinline__ bool Walk<1>::set(const ScoresBwdArgs &a, const BwPla
 struct BwSmem {
     uint64_t a_full[2], a_empty[2];
     uint64_t b_full[kBwRing], b_empty[kBwRing];
-    uint64_t c_empty[2];                 // fp16 tiles
-    uint64_t s_full[2];                  // per stationary tile: products there
-    uint64_t m_full[3];                  // M there; of the first tile B2 too (even steps, odd steps), of the second
+    uint64_t c_empty[2];                 // fp16 tiles read
+    uint64_t s_full[2][2];               // per stationary tile and half: products there
+    uint64_t m_full[2][2][2];            // per tile and half, even and odd steps: M and B2 there
     uint64_t acc_full[2];
-    uint64_t drain;
+    uint64_t g_full[2], g_empty[2];      // dq: gk staged, read
+    uint64_t dw_full[2];                 // dq, per tile: the second half's part of dw
+    float dw[2][128];
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort_flag;
 };
 
+// dq: gk of two steps, both tiles; and 1 KB of output for each epilogue warp.
+constexpr size_t gk_bytes(int hp) { return (size_t)2 * 2 * (128 / hp) * gk_row(hp) * 4; }
+
 template <int D>
-constexpr size_t bw_smem_bytes(bool dq)
+constexpr size_t bw_smem_bytes(bool dq, int hp)
 {
-    return 1024 + 4 * 128 * D + (size_t)kBwRing * 128 * D + 2 * 128 * D * 2 +
-           (dq ? 2 * 2 * (size_t)kBwMaxTok * kBwRow * 4 + 8 * 2048 : 0) + sizeof(BwSmem);
+    return 1024 + 4 * 128 * D + (size_t)kBwRing * 128 * D + 2 * 128 * D * 2 + (dq ? gk_bytes(hp) + 16 * 1024 : 0) +
+           sizeof(BwSmem);
 }
+static_assert(bw_smem_bytes<128>(true, 8) <= 232448, "shared memory of a block");
 
 // Offset of 16-byte chunk c of row r in a tile of ROW_BYTES rows stored with
 // the swizzle of that span (rows of 32, 64 or 128 bytes; the 16-byte chunks
@@ -321,33 +334,40 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int TT = 128 / HP;                       // tokens of a 128-row tile
+    constexpr int kBwRow = gk_row(HP);
     constexpr uint32_t tile8 = 128 * D, tile16 = 256 * D;
     constexpr int kC = D * 2 > 128 ? 128 : D * 2;      // bytes of a row block of the fp16 tile
     uint8_t *sa = base;                                // [2 items][2 tiles]
     uint8_t *sb = sa + 4 * tile8;                      // [ring]
     uint8_t *sc = sb + kBwRing * tile8;                // [2] fp16
-    float *sg = reinterpret_cast<float *>(sc + 2 * tile16);   // dq: [2 tiles][2][kBwMaxTok][kBwRow] gk,
-                                                              // then 2 KB of output a warp
+    float *sg = reinterpret_cast<float *>(sc + 2 * tile16);   // dq: [2][2 TT][kBwRow] gk,
+                                                              // then 1 KB of output a warp
     BwSmem *sm = reinterpret_cast<BwSmem *>(reinterpret_cast<uint8_t *>(sg) +
-                                            (MODE == 0 ? 4 * kBwMaxTok * kBwRow * 4 + 8 * 2048 : 0));
-    const int warp = threadIdx.x >> 5;
+                                            (MODE == 0 ? gk_bytes(HP) + 16 * 1024 : 0));
+    constexpr int kConv = MODE == 0 ? 4 : 8;           // converting warps
+    const int warp = uniform_warp();
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->a_full[i], 1);
-            mbar_init(&sm->a_empty[i], 1);
-            mbar_init(&sm->c_empty[i], 1);
-            mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->m_full[i], 4 + 4);       // the epilogue's warps and the converters, who run a step ahead
+            mbar_init(&sm->a_empty[i], 2);          // each tile's last products
+            mbar_init(&sm->c_empty[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm->s_full[i][h], 1);
+                mbar_init(&sm->m_full[i][h][0], 4 + kConv);    // the epilogue's warps and the converters
+                mbar_init(&sm->m_full[i][h][1], 4 + kConv);
+            }
             mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->g_full[i], 4);
+            mbar_init(&sm->g_empty[i], 16);
+            mbar_init(&sm->dw_full[i], 4);
+            mbar_init(&sm->drain[i], 1);
         }
         for (int i = 0; i < kBwRing; ++i) {
             mbar_init(&sm->b_full[i], 1);
-            mbar_init(&sm->b_empty[i], 1 + 4);      // products done (passed on by a warp); converted
+            mbar_init(&sm->b_empty[i], 4 + kConv);  // all products done (passed on by warps); converted
         }
-        mbar_init(&sm->m_full[2], 4);
-        mbar_init(&sm->drain, 1);
         sm->abort_flag = 0;
         fence_mbar_init();
     }
@@ -423,110 +443,121 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        // One thread runs this role alone: a wait or a commit costs it about 150
-        // cycles, so it has three waits and two commits a step; everything else
-        // that must be known done (code tiles read, fp16 tiles read) follows from
-        // the second tile's products of the next step and is passed on by the
-        // warps that wait for those.
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_i8_s32(128, 128);
-            constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
-            int stage = 0, item = -1, n = 0;
-            uint32_t phase = 0;
-            bool issued = false;
-            auto products = [&](int i) {
-                // S_i = A_i B^T of the walk's step
-                const uint64_t da = sdesc_k_rows<D>(smem_u32(sa + (2 * (item & 1) + i) * tile8));
-                const uint64_t db = sdesc_k_rows<D>(smem_u32(sb + stage * tile8));
+    } else if (warp == 1 || warp == 2) {
+        // ------------------------------------------------ MMA issuer of tile i
+        // A wait or a commit costs a warp about 100 cycles, so a step has two
+        // waits and one commit; everything else that must be known done (code tiles
+        // read, fp16 tiles read) follows from the products of the next step and
+        // is passed on by the warps that wait for those. The halves are added in order.
+        const int i = warp - 1;
+        constexpr uint32_t id_s = idesc_i8_s32(128, 64);
+        constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
+        const uint64_t a_desc = sdesc_k_rows<D>(smem_u32(sa + i * tile8));
+        const uint64_t b_desc = sdesc_k_rows<D>(smem_u32(sb));
+        const uint64_t c_desc = sdesc_mn_rows<kC>(smem_u32(sc), 128 * kC);
+        const uint32_t t_s = tmem + i * 128, t_acc = tmem + 256 + i * D;
+        int stage = 0, item = -1, n = 0;
+        uint32_t phase = 0;
+        bool issued = false;
+        // S = A B^T of the walk's step, for the 64 rows of B that half `hf` names
+        auto products = [&](int hf) {
+            const uint64_t da = a_desc + 2 * (item & 1) * (tile8 / 16);
+            const uint64_t db = b_desc + stage * (tile8 / 16) + hf * (tile8 / 32);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
-                    umma_i8(tmem + i * 128, da + 2 * kk, db + 2 * kk, id_s, kk != 0);
-                umma_commit(&sm->s_full[i]);
-            };
-            // the walk's step: its tiles are in place
-            auto arrive_step = [&]() -> bool {
-                if (wk.first) {
-                    ++item;
-                    if (!mbar_wait_short(&sm->a_full[item & 1], (item >> 1) & 1, abort_flag, a.err))
-                        return false;
-                }
-                return mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err);
-            };
-            auto done_step = [&]() {
-                if (wk.last())
+                    umma_i8(t_s + hf * 64, da + 2 * kk, db + 2 * kk, id_s, kk != 0);
+                umma_commit(&sm->s_full[i][hf]);
+                if (hf == 1 && wk.last())
                     umma_commit(&sm->a_empty[item & 1]);
-                if (++stage == kBwRing) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            };
-            bool go = wk.begin(a, p), ok = true;
-            if (go) {
-                ok = arrive_step();
-                if (ok) {
-                    tc_fence_after();
-                    products(0);
-                    products(1);
-                    issued = true;
-                    done_step();
-                }
             }
-            while (go && ok) {
-                const bool fresh = wk.first, closes = wk.last();
-                const uint64_t dc = sdesc_mn_rows<kC>(smem_u32(sc + (n & 1) * tile16), 128 * kC);
-                go = wk.next(a, p);                  // the walk is now one step ahead
-                if (go && !arrive_step())
+            __syncwarp();
+            issued = true;
+            if (hf == 1 && ++stage == kBwRing) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        // the walk's step: its tiles are in place
+        auto arrive_step = [&]() -> bool {
+            if (wk.first) {
+                ++item;
+                if (!warp_mbar_wait_short(&sm->a_full[item & 1], (item >> 1) & 1, abort_flag, a.err))
+                    return false;
+            }
+            return warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err);
+        };
+        bool go = wk.begin(a, p);
+        bool ok = go && arrive_step();
+        if (ok) {
+            tc_fence_after();
+            products(0);
+            products(1);
+        }
+        while (go && ok) {
+            const bool fresh = wk.first, closes = wk.last();
+            const uint64_t dc = c_desc + (n & 1) * (tile16 / 16);
+            go = wk.next(a, p);                  // the walk is now one step ahead
+            ok = !go || arrive_step();
+#pragma unroll
+            for (int hf = 0; hf < 2 && ok; ++hf) {
+                ok = warp_mbar_wait_short(&sm->m_full[i][hf][n & 1], (n >> 1) & 1, abort_flag, a.err);
+                if (!ok)
                     break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ok = i == 0 ? mbar_wait_short(&sm->m_full[n & 1], (n >> 1) & 1, abort_flag, a.err)
-                                : mbar_wait_short(&sm->m_full[2], n & 1, abort_flag, a.err);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_f16_ta(tmem + 256 + i * D, tmem + i * 128 + kk * 8, dc + kk * kC, id_acc,
-                                    (kk != 0 || !fresh) ? 1u : 0u);
-                    if (closes)
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ta(t_acc, t_s + hf * 64 + kk * 8, dc + (hf * 4 + kk) * kC, id_acc,
+                                    hf == 0 && kk == 0 && fresh ? 0u : 1u);
+                    if (hf == 1 && closes)
                         umma_commit(&sm->acc_full[i]);
-                    if (go)
-                        products(i);
                 }
-                if (ok && go)
-                    done_step();
-                ++n;
+                __syncwarp();
+                if (go)
+                    products(hf);
             }
-            if (*abort_flag && issued) {
-                umma_commit(&sm->drain);
-                mbar_drain(&sm->drain, 0);
-            }
+            ++n;
+        }
+        if (*abort_flag && issued && lane == 0) {
+            umma_commit(&sm->drain[i]);
+            mbar_drain(&sm->drain[i], 0);
         }
         __syncwarp();
-    } else if (warp >= 12) {
+    } else if (warp >= 20 && warp < 20 + kConv) {
         // ------------------------------------------------ codes to fp16
-        const int r = threadIdx.x - 384;               // row of the tile
+        const int r = (threadIdx.x - 640) & 127;       // row of the tile; dk: two threads a row
+        constexpr int kChunks = D / 16 / (kConv / 4);  // 16-code chunks a thread
+        const int chunk0 = MODE == 0 ? 0 : ((threadIdx.x - 640) >> 7) * kChunks;
         const float fw = MODE == 1 ? range_scale(__ldg(p.max + kMaxW), 8) : 1.f;
-        // dk: this row's scale, loaded a step ahead
-        auto scale_of = [&](int s) -> float {
+        // dk: this row's scale; its parts are loaded a step ahead and put together when used
+        float rw = 0.f, rs = 0.f;
+        uint32_t ra = 0;
+        auto fetch = [&]() {
+            if (MODE == 0)
+                return;
             const int tt = r / HP, h = r % HP;
-            const int t = s * TT + tt;
-            if (t >= a.S || h >= a.H)
-                return 0.f;
-            const int64_t row = (int64_t)wk.b * a.S + t;
-            if (__ldg(p.row + row) == 0u)
-                return 0.f;                            // no gradient: whatever w holds, the row adds nothing
-            return __ldg(a.w + row * a.H + h) * __ldg(a.q_scale + row * a.H + h) * fw;
+            const int t = wk.s * TT + tt;
+            ra = 0;
+            rw = rs = 0.f;
+            if (t < a.S && h < a.H) {
+                const int64_t row = (int64_t)wk.b * a.S + t;
+                ra = __ldg(p.row + row);
+                rw = __ldg(a.w + row * a.H + h);
+                rs = __ldg(a.q_scale + row * a.H + h);
+            }
         };
         int stage = 0, n = 0;
         uint32_t phase = 0;
         bool go = wk.begin(a, p);
-        float scale = MODE == 1 && go ? scale_of(wk.s) : 1.f;
+        if (go)
+            fetch();
         while (go) {
+            // (a token without a gradient adds nothing, whatever its weights hold)
+            const float scale = MODE == 1 ? (ra ? rw * rs * fw : 0.f) : 1.f;
             go = wk.next(a, p);
-            const float next_scale = MODE == 1 && go ? scale_of(wk.s) : 1.f;
+            if (go)
+                fetch();
             const int cb = n & 1;
             if (!warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err) ||
                 !warp_mbar_wait_short(&sm->c_empty[cb], ((n >> 1) & 1) ^ 1u, abort_flag, a.err))
@@ -539,7 +570,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
             const __half2 off = __floats2half2_rn(-1152.f, -1152.f);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+            for (int k = 0; k < kChunks; ++k) {
+                const int c = chunk0 + k;
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + swz<D>(r, c));
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[8];
@@ -566,27 +598,74 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sm->m_full[cb]);
+                for (int i = 0; i < 4; ++i)
+                    mbar_arrive(&sm->m_full[i >> 1][i & 1][cb]);
                 mbar_arrive(&sm->b_empty[stage]);
             }
-            scale = next_scale;
             ++n;
             if (++stage == kBwRing) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
+    } else if (MODE == 0 && warp >= 24) {
+        // ------------------------------------------------ dq: gk staged
+        // gk of the step's 128 keys and both tiles' tokens: thread = key, one value
+        // a token, read from G a step ahead; lane e holds token e's candidates.
+        constexpr int NT = 2 * TT;
+        const int r = threadIdx.x - 768;
+        const float f = range_scale(__ldg(p.max + kMaxGk), 15);
+        float g[NT], ksv = 0.f;
+        int lo = 0, hi = 0;
+        auto fetch = [&]() {
+            if (wk.first) {
+                const int t = wk.a0 + lane;
+                lo = hi = 0;
+                if (lane < NT && t < a.S)
+                    token_range(a, wk.b, t, lo, hi);
+            }
+            const int j = wk.s * 128 + r;
+            ksv = j < a.P ? __ldg(a.k_scale + (int64_t)wk.b * a.P + j) : 0.f;
+            const float *src = p.G + ((int64_t)wk.b * a.S + wk.a0) * a.P + j;
+#pragma unroll
+            for (int e = 0; e < NT; ++e, src += a.P) {
+                const int l = __shfl_sync(0xffffffffu, lo, e), u = __shfl_sync(0xffffffffu, hi, e);
+                g[e] = j >= l && j < u ? __ldg(src) : 0.f;
+            }
+        };
+        int n = 0;
+        bool go = wk.begin(a, p);
+        if (go)
+            fetch();
+        while (go) {
+            if (!warp_mbar_wait_short(&sm->g_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag, a.err))
+                break;
+            float *dst = sg + (n & 1) * NT * kBwRow + r;
+#pragma unroll
+            for (int e = 0; e < NT; ++e)
+                dst[e * kBwRow] = g[e] != 0.f ? g[e] * ksv * f : 0.f;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm->g_full[n & 1]);
+            ++n;
+            go = wk.next(a, p);
+            if (go)
+                fetch();
+        }
     } else if (warp >= 4) {
-        // ------------------------------------------------ epilogue of tile i
-        const int i = (warp - 4) >> 2;
+        // ------------------------------------------------ epilogue of tile i, 64 columns a warp
+        const int i = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
         const int q = warp & 3;
         const int r = q * 32 + lane;                   // tile row
-        const uint32_t ts = tmem + i * 128 + ((uint32_t)(q * 32) << 16);
-        // One warp of the second tile passes on what its products of step n imply:
-        // step n's code tile and step n-1's fp16 tile have been read.
+        // S columns [64 half, 64 half + 64); M takes the first 32 of them
+        const uint32_t ts = tmem + i * 128 + half * 64 + ((uint32_t)(q * 32) << 16);
+        // the accumulator's columns that this warp reads
+        const uint32_t ta = tmem + 256 + i * D + half * (D / 2) + ((uint32_t)(q * 32) << 16);
+        // One warp passes on what its tile's products of step n imply: it has read
+        // step n's code tile and step n-1's fp16 tile.
         int ring = 0;
         auto pass_on = [&](int n) {
-            if (i == 1 && q == 0 && lane == 0) {
+            if (q == 0 && lane == 0) {
                 mbar_arrive(&sm->b_empty[ring]);
                 if (n > 0)
                     mbar_arrive(&sm->c_empty[(n - 1) & 1]);
@@ -594,205 +673,217 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             if (++ring == kBwRing)
                 ring = 0;
         };
-        const uint32_t ta = tmem + 256 + i * D + ((uint32_t)(q * 32) << 16);
+        int n = 0, items = 0;
         if constexpr (MODE == 0) {
-            const float f = range_scale(__ldg(p.max + kMaxGk), 15);
-            const float inv = 1.f / f;
+            const float inv = 1.f / range_scale(__ldg(p.max + kMaxGk), 15);
             const int tt = r / HP, h = r % HP;
-            float *stage0 = sg + i * 2 * kBwMaxTok * kBwRow;
-            uint4 *out = reinterpret_cast<uint4 *>(sg + 4 * kBwMaxTok * kBwRow) + (warp - 4) * 128;
+            uint4 *out = reinterpret_cast<uint4 *>(sg + 4 * TT * kBwRow) + (warp - 4) * 64;
             // Items without a candidate never reach the walk: their gradients are zero.
             for (int it = (int)blockIdx.x; it < a.B * p.n_pairs; it += gridDim.x) {
                 const int b = it % a.B, a0 = (p.n_pairs - 1 - it / a.B) * 2 * TT, t = a0 + i * TT + tt;
-                if (((uint32_t)a.t_begin + (uint32_t)min(a.S, a0 + 2 * TT)) / (uint32_t)a.cr > 0 || t >= a.S || h >= a.H)
+                if (((uint32_t)a.t_begin + (uint32_t)min(a.S, a0 + 2 * TT)) / (uint32_t)a.cr > 0 || t >= a.S || h >= a.H || half)
                     continue;
                 const int64_t row = ((int64_t)b * a.S + t) * a.H + h;
                 a.dw[row] = 0.f;
                 for (int c = 0; c < D / 8; ++c)
                     reinterpret_cast<uint4 *>(a.dq + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
             }
-            // gk of the step's 128 keys and this tile's tokens: thread = key, one value a token;
-            // lane e holds token e's candidates
-            float g[TT], ksv = 0.f;
-            int lo = 0, hi = 0;
-            auto bounds = [&]() {
-                const int t = wk.a0 + i * TT + lane;
-                lo = hi = 0;
-                if (lane < TT && t < a.S)
-                    token_range(a, wk.b, t, lo, hi);
-            };
-            auto fetch = [&]() {
-                const int j = wk.s * 128 + r;
-                ksv = j < a.P ? __ldg(a.k_scale + (int64_t)wk.b * a.P + j) : 0.f;
-                const float *src = p.G + ((int64_t)wk.b * a.S + wk.a0 + i * TT) * a.P + j;
-#pragma unroll
-                for (int e = 0; e < TT; ++e) {
-                    const int l = __shfl_sync(0xffffffffu, lo, e), u = __shfl_sync(0xffffffffu, hi, e);
-                    g[e] = j >= l && j < u ? __ldg(src + (int64_t)e * a.P) : 0.f;
+            // The thread's row of the current item, and of a finished one whose
+            // accumulator is still to be read: that is done after the next item's
+            // first M is formed (its products were under way), just before M is
+            // handed over, from when on the accumulator may be overwritten.
+            constexpr uint32_t kNone = 0xffffffffu;
+            uint32_t row = kNone, old_row = kNone;      // B S H fits 31 bits
+            float wq = 0.f, qs = 0.f, old_wq = 0.f, old_dw = 0.f;
+            bool any = false, old_any = false, pending = false;
+            uint64_t dw[2] = {0u, 0u};                  // two fp32 sums each
+            auto finish = [&]() -> bool {
+                if (half) {
+                    sm->dw[i][r] = old_dw;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm->dw_full[i]);
                 }
-            };
-            auto put = [&](int buf) {
+                if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err) ||
+                    (!half && !warp_mbar_wait_short(&sm->dw_full[i], items & 1, abort_flag, a.err)))
+                    return false;
+                ++items;
+                pending = false;
+                tc_fence_after();
+                if (!half && old_row != kNone)
+                    a.dw[old_row] = old_any ? old_dw + sm->dw[i][r] : 0.f;
+                // 16 values of the warp's 32 rows at a time, through shared memory: two
+                // lanes store one row's 32 bytes, not 32 lanes 16 bytes of 32 rows
+                uint32_t dst[2];
 #pragma unroll
-                for (int e = 0; e < TT; ++e)
-                    stage0[(buf * kBwMaxTok + e) * kBwRow + r] = g[e] != 0.f ? g[e] * ksv * f : 0.f;
+                for (int e = 0; e < 2; ++e)
+                    dst[e] = __shfl_sync(0xffffffffu, old_row, e * 16 + (lane >> 1));
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(ta + c, v);
+                    tmem_ld_wait();
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y0 = __uint_as_float(v[u * 8 + 2 * e]) * old_wq;
+                            const float y1 = __uint_as_float(v[u * 8 + 2 * e + 1]) * old_wq;
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
+                            o[e] = old_any ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
+                        }
+                        out[lane * 2 + (u ^ ((lane >> 2) & 1))] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int l = e * 16 + (lane >> 1), u = lane & 1;
+                        const uint4 o = out[l * 2 + (u ^ ((l >> 2) & 1))];
+                        if (dst[e] != kNone)
+                            *reinterpret_cast<uint4 *>(a.dq + (int64_t)dst[e] * D + half * (D / 2) + c + u * 8) = o;
+                    }
+                }
+                return true;
             };
-            int n = 0, items = 0;
             bool go = wk.begin(a, p), ok = true;
-            if (go) {
-                bounds();
-                fetch();
-            }
-            float dw[4] = {0.f, 0.f, 0.f, 0.f};
-            while (go) {
-                put(n & 1);
-                // a wait that gave up ends the loop here, for the four warps together
-                if (!named_bar_and(1 + i, 128, ok))
-                    break;
-                const Walk<MODE> me = wk;
+            while (go && ok) {
+                if (wk.first) {
+                    const int t = wk.a0 + i * TT + tt;
+                    row = t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
+                    any = row != kNone && __ldg(p.row + (int64_t)wk.b * a.S + t) != 0u;
+                    wq = row != kNone ? __ldg(a.w + row) * inv : 0.f;
+                    qs = row != kNone ? __ldg(a.q_scale + row) * inv : 0.f;
+                }
                 const bool closes = wk.last();
                 go = wk.next(a, p);
-                if (go) {
-                    if (wk.first)
-                        bounds();
-                    fetch();                            // the next step's, in flight during this one
-                }
-                if (!warp_mbar_wait_short(&sm->s_full[i], n & 1, abort_flag, a.err)) {
-                    ok = false;
-                    continue;
-                }
+                if (!warp_mbar_wait_short(&sm->g_full[n & 1], (n >> 1) & 1, abort_flag, a.err) ||
+                    !warp_mbar_wait_short(&sm->s_full[i][half], n & 1, abort_flag, a.err))
+                    break;
                 pass_on(n);
                 tc_fence_after();
-                const float *gk = stage0 + ((n & 1) * kBwMaxTok + tt) * kBwRow;
-                uint32_t x[2][16];
-                tmem_ld16(ts, x[0]);
+                const float *gk = sg + ((n & 1) * 2 * TT + i * TT + tt) * kBwRow + half * 64;
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
-                    const uint32_t(&v)[16] = x[(c / 16) & 1];
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(ts + c, v);
                     tmem_ld_wait();
-                    if (c + 16 < 128)
-                        tmem_ld16(ts + c + 16, x[(c / 16 + 1) & 1]);
                     uint32_t m[8];
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
                         const float4 w = *reinterpret_cast<const float4 *>(gk + c + e);
-                        const float wv[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t on[4];
+                        // relu and conversion in one: max(x + M, M), M the bits of 2^23
+                        float y[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            on[u] = (uint32_t)__vimin_s32_relu((int)v[e + u], 1);
-                            dw[u] = fmaf(__int_as_float(__viaddmax_s32((int)v[e + u], 0x4B000000, 0x4B000000)) -
-                                             8388608.f,
-                                         wv[u], dw[u]);
-                        }
+                        for (int u = 0; u < 4; ++u)
+                            y[u] = __int_as_float(__viaddmax_s32((int)v[e + u], 0x4B000000, 0x4B000000));
+                        const uint64_t y01 = add2(pack2(y[0], y[1]), pack2(-8388608.f, -8388608.f));
+                        const uint64_t y23 = add2(pack2(y[2], y[3]), pack2(-8388608.f, -8388608.f));
+                        dw[0] = fma2(y01, pack2(w.x, w.y), dw[0]);
+                        dw[1] = fma2(y23, pack2(w.z, w.w), dw[1]);
+                        unpack2(y01, y[0], y[1]);
+                        unpack2(y23, y[2], y[3]);
+                        // m as a mask of 16 bits a value (y is 0 or at least 1)
                         const __half2 h01 = __floats2half2_rn(w.x, w.y), h23 = __floats2half2_rn(w.z, w.w);
-                        m[e / 2] = *reinterpret_cast<const uint32_t *>(&h01) & ((on[0] + (on[1] << 16)) * 0xffffu);
-                        m[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h23) & ((on[2] + (on[3] << 16)) * 0xffffu);
+                        const __half2 zero = __half2half2(__ushort_as_half(0));
+                        m[e / 2] = *reinterpret_cast<const uint32_t *>(&h01) &
+                                   __hgt2_mask(__floats2half2_rn(y[0], y[1]), zero);
+                        m[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h23) &
+                                       __hgt2_mask(__floats2half2_rn(y[2], y[3]), zero);
                     }
                     tmem_st8(ts + c / 2, m);            // these columns have been read
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->g_empty[n & 1]);
+                if (pending)
+                    ok = finish();
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sm->m_full[i == 0 ? n & 1 : 2]);
+                    mbar_arrive(&sm->m_full[i][half][n & 1]);
                 ++n;
                 if (closes) {
-                    if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err)) {
-                        ok = false;
-                        continue;
-                    }
-                    ++items;
-                    tc_fence_after();
-                    const int t = me.a0 + i * TT + tt;
-                    const bool mine = t < a.S && h < a.H;
-                    const int64_t trow = (int64_t)me.b * a.S + (mine ? t : 0);
-                    const int64_t row = trow * a.H + (mine ? h : 0);
-                    const bool any = mine && __ldg(p.row + trow) != 0u;
-                    const float wq = any ? __ldg(a.w + row) * inv : 0.f;
-                    if (mine)
-                        a.dw[row] = any ? ((dw[0] + dw[1]) + (dw[2] + dw[3])) * inv * __ldg(a.q_scale + row) : 0.f;
-                    dw[0] = dw[1] = dw[2] = dw[3] = 0.f;
-                    // 32 values of the warp's 32 rows at a time, through shared memory: four
-                    // lanes store one row's 64 bytes, not 32 lanes 16 bytes of 32 rows
-                    const uint32_t my_row = mine ? (uint32_t)row : 0xffffffffu;     // B S H fits 31 bits
-                    uint32_t dst[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = __shfl_sync(0xffffffffu, my_row, e * 8 + (lane >> 2));
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t v[2][16];
-                        tmem_ld16(ta + c, v[0]);
-                        tmem_ld16(ta + c + 16, v[1]);
-                        tmem_ld_wait();
-                        __syncwarp();
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float y0 = any ? __uint_as_float(v[u / 2][(u % 2) * 8 + 2 * e]) * wq : 0.f;
-                                const float y1 = any ? __uint_as_float(v[u / 2][(u % 2) * 8 + 2 * e + 1]) * wq : 0.f;
-                                const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
-                                o[e] = *reinterpret_cast<const uint32_t *>(&y);
-                            }
-                            out[lane * 4 + (u ^ ((lane >> 1) & 3))] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int l = e * 8 + (lane >> 2), u = lane & 3;
-                            const uint4 o = out[l * 4 + (u ^ ((l >> 1) & 3))];
-                            if (dst[e] != 0xffffffffu)
-                                *reinterpret_cast<uint4 *>(a.dq + (int64_t)dst[e] * D + c + u * 8) = o;
-                        }
-                    }
-                    tc_fence_before();
+                    pending = true;
+                    old_row = row;
+                    old_any = any;
+                    old_wq = wq;
+                    float d0, d1;
+                    unpack2(add2(dw[0], dw[1]), d0, d1);
+                    old_dw = any ? (d0 + d1) * qs : 0.f;
+                    dw[0] = dw[1] = 0u;
                 }
             }
+            if (pending && ok)
+                finish();
         } else {
             const float fg = range_scale(__ldg(p.max + kMaxG), 15);
             const float inv = 1.f / fg, inv_w = 1.f / range_scale(__ldg(p.max + kMaxW), 8);
-            // this key's gradients of the step's tokens, as fp16 bits, loaded a step ahead
-            uint32_t g[TT];
-            float raw[TT];
+            // this key's gradients of the tokens of the warp's columns, read a step
+            // ahead; lane e holds token e's candidates, [0, hi) kept up by counting
+            constexpr int NT = HP > 64 ? 1 : TT / 2;    // tokens of 64 columns
+            const int e0 = HP > 64 ? 0 : half * NT;
+            float raw[NT];
+            int lo = 0, hi = 0, rem = 0;
+            const int up = TT / a.cr, up_rem = TT - up * a.cr;
             auto fetch = [&]() {
                 const int j = wk.a0 + i * 128 + r;
-                const int t0 = wk.s * TT;
-                int lo = 0, hi = 0;
-                if (lane < TT && t0 + lane < a.S)
-                    token_range(a, wk.b, t0 + lane, lo, hi);
-                const float *src = p.G + ((int64_t)wk.b * a.S + t0) * a.P + j;
+                const int t = wk.s * TT + lane;
+                if (wk.first) {
+                    const uint32_t ends = (uint32_t)a.t_begin + (uint32_t)t + 1u;
+                    hi = (int)(ends / (uint32_t)a.cr);
+                    rem = (int)(ends - (uint32_t)hi * (uint32_t)a.cr);
+                } else {
+                    hi += up;
+                    rem += up_rem;
+                    if (rem >= a.cr) {
+                        rem -= a.cr;
+                        ++hi;
+                    }
+                }
+                const float *src = p.G + ((int64_t)wk.b * a.S + wk.s * TT + e0) * a.P + j;
+                const int end = t < a.S ? min(a.P, hi) : 0;
+                if (a.doc_start) {
+                    int l, u;
+                    lo = 0;
+                    if (lane < TT && t < a.S) {
+                        token_range(a, wk.b, t, l, u);
+                        lo = l;
+                    }
+                }
 #pragma unroll
-                for (int e = 0; e < TT; ++e) {
-                    const int l = __shfl_sync(0xffffffffu, lo, e), u = __shfl_sync(0xffffffffu, hi, e);
-                    raw[e] = j >= l && j < u ? __ldg(src + (int64_t)e * a.P) : 0.f;
+                for (int e = 0; e < NT; ++e, src += a.P) {
+                    const int u = __shfl_sync(0xffffffffu, end, e0 + e), l = __shfl_sync(0xffffffffu, lo, e0 + e);
+                    raw[e] = j >= l && j < u ? __ldg(src) : 0.f;
                 }
             };
-            int n = 0, items = 0;
             bool go = wk.begin(a, p);
             if (go)
                 fetch();
             while (go) {
+                uint32_t g[NT];
 #pragma unroll
-                for (int e = 0; e < TT; ++e)
+                for (int e = 0; e < NT; ++e)
                     g[e] = __half_as_ushort(__float2half_rn(raw[e] * fg));
-                const Walk<MODE> me = wk;
+                const int pair = wk.pair;
                 const bool closes = wk.last();
                 go = wk.next(a, p);
                 if (go)
                     fetch();
-                if (!warp_mbar_wait_short(&sm->s_full[i], n & 1, abort_flag, a.err))
+                if (!warp_mbar_wait_short(&sm->s_full[i][half], n & 1, abort_flag, a.err))
                     break;
                 pass_on(n);
                 tc_fence_after();
+                // 16 columns at a time; the next 16 are loaded while these are masked
                 uint32_t x[2][16];
                 tmem_ld16(ts, x[0]);
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < 64; c += 16) {
                     const uint32_t(&v)[16] = x[(c / 16) & 1];
                     tmem_ld_wait();
-                    if (c + 16 < 128)
+                    if (c + 16 < 64)
                         tmem_ld16(ts + c + 16, x[(c / 16 + 1) & 1]);
                     uint32_t m[8];
 #pragma unroll
@@ -800,7 +891,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                         // (1 or 0, 1 or 0) times the token's 16 bits
                         const uint32_t on = (uint32_t)__vimin_s32_relu((int)v[2 * e], 1) +
                                             ((uint32_t)__vimin_s32_relu((int)v[2 * e + 1], 1) << 16);
-                        m[e] = on * g[(c + 2 * e) / HP];
+                        m[e] = on * g[HP > 64 ? 0 : (c + 2 * e) / HP];
                     }
                     tmem_st8(ts + c / 2, m);            // these columns have been read
                 }
@@ -808,7 +899,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sm->m_full[i == 0 ? n & 1 : 2]);
+                    mbar_arrive(&sm->m_full[i][half][n & 1]);
                 ++n;
                 if (closes) {
                     if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
@@ -816,9 +907,9 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                     ++items;
                     tc_fence_after();
                     // segment of pair `pair` in this CTA's share: both count up, their sum names it
-                    float *o = p.part + ((int64_t)(blockIdx.x + me.pair) * 256 + i * 128 + r) * D;
+                    float *o = p.part + ((int64_t)((int)blockIdx.x + pair) * 256 + i * 128 + r) * D + half * (D / 2);
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < D / 2; c += 16) {
                         uint32_t v[16];
                         tmem_ld16(ta + c, v);
                         tmem_ld_wait();
@@ -900,15 +991,15 @@ cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, 
         !make_map_q8(&keys, a.k8, D, a.P, a.B, 128, 1))
         return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel<0, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bw_smem_bytes<D>(true));
+                                         (int)bw_smem_bytes<D>(true, HP));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(bwd_tc_kernel<1, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)bw_smem_bytes<D>(false));
+                                 (int)bw_smem_bytes<D>(false, HP));
     if (e != cudaSuccess)
         return e;
-    bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true), st>>>(rows, keys, a, pq);
+    bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true, HP), st>>>(rows, keys, a, pq);
     if (grid_k > 0)
-        bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false), st>>>(keys, rows, a, pk);
+        bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false, HP), st>>>(keys, rows, a, pk);
     bwd_reduce_kernel<<<(unsigned)(a.B * pk.n_pairs * (D / 4)), 256, 0, st>>>(a, pk, grid_k);
     return cudaGetLastError();
 }

@@ -29,6 +29,27 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
+// This thread's warp within the block, in a form that the compiler knows to be
+// the same for the whole warp: what a role derives from it (loop counters,
+// descriptors) then stays in uniform registers, where the tensor-core
+// instructions want it.
+__device__ __forceinline__ int uniform_warp()
+{
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)
 {
@@ -345,6 +366,30 @@ __device__ __forceinline__ uint64_t sdesc_mn_rows(uint32_t saddr, uint32_t block
     d |= (uint64_t)((8 * N_BYTES) >> 4) << 32;         // stride byte offset: 8 rows of K
     d |= (uint64_t)1 << 46;                            // descriptor version (sm_100)
     d |= layout << 61;
+    return d;
+}
+
+// Two fp32 operations in one instruction, each rounded as the single one is.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
 
