@@ -152,6 +152,8 @@ def _call(fn, dev: torch.device, *args) -> int:
     takes its device (SM count, TMA encoding, the allocation-free call's
     scratch array) from the current device, and the stream passed is that
     device's current stream."""
+    if dev.index == torch.cuda.current_device():   # (switching and back costs more than a small launch)
+        return fn(*args, _stream(dev))
     with torch.cuda.device(dev):
         return fn(*args, _stream(dev))
 

@@ -59,8 +59,8 @@ constexpr int kBwRing = 3;              // code tiles B in flight
 // span few tokens, so that they use other banks (with 16 tokens a tile the shared
 // memory has no room for it).
 constexpr int gk_row(int hp) { return hp == 8 ? 128 : 132; }
-constexpr int kPrepThreads = 256;
-constexpr int kPrepCols = 4096;         // columns of G gathered at once
+constexpr int kPrepThreads = 128;
+constexpr int kPrepCols = 4096;         // columns of G gathered at once, at most
 
 // Largest magnitudes, as bits: |G ks|, |G|, |w qs| of tokens with a gradient.
 enum { kMaxGk = 0, kMaxG = 1, kMaxW = 2, kMaxWords = 4 };
@@ -108,10 +108,11 @@ __device__ __forceinline__ void token_range(const ScoresBwdArgs &a, int b, int t
 // bit; if any block is claimed twice, the columns are gathered again by one
 // thread a block in slot order, so that the sum does not depend on timing.
 __global__ void __launch_bounds__(kPrepThreads)
-    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any)
+    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any, bool vec, int cols)
 {
-    __shared__ float g[kPrepCols];
-    __shared__ uint32_t claimed[kPrepCols / 32];
+    extern __shared__ float4 prep_smem[];            // [cols] G, [cols / 32] claims
+    float *g = reinterpret_cast<float *>(prep_smem);
+    uint32_t *claimed = reinterpret_cast<uint32_t *>(g + cols);
     __shared__ uint32_t buf[4][kPrepThreads / 32];
     const int64_t row = blockIdx.x;
     const int b = (int)(row / a.S);
@@ -126,38 +127,70 @@ __global__ void __launch_bounds__(kPrepThreads)
     uint32_t top[4] = {0u, 0u, 0u, 0u};              // kMaxGk, kMaxG, kMaxW; any gradient at all
     const float *ks = a.k_scale + (int64_t)b * a.P;
     const float *ds = a.dscores + row * a.K;
-    auto seen = [&](float v, int j) {
+    auto seen = [&](float v, float scale) {
         if (v != 0.f) {
             top[3] = 1u;
             top[kMaxG] = max(top[kMaxG], finite(v));
-            top[kMaxGk] = max(top[kMaxGk], finite(v * __ldg(ks + j)));
+            top[kMaxGk] = max(top[kMaxGk], finite(v * scale));
         }
     };
-    for (int h = threadIdx.x; h < a.H; h += kPrepThreads)
-        top[kMaxW] = max(top[kMaxW], finite(__ldg(a.w + row * a.H + h) * __ldg(a.q_scale + row * a.H + h)));
+    // (H <= 128: one value a thread, loaded ahead)
+    const bool has_h = (int)threadIdx.x < a.H;
+    const float wv = has_h ? __ldg(a.w + row * a.H + threadIdx.x) : 0.f;
+    const float qv = has_h ? __ldg(a.q_scale + row * a.H + threadIdx.x) : 0.f;
     if (!a.idx) {
         for (int j = lo + threadIdx.x; j < hi; j += kPrepThreads)
-            seen(__ldg(ds + j), j);
+            seen(__ldg(ds + j), __ldg(ks + j));
     } else {
         const int32_t *idx = a.idx + row * a.K;
-        for (int c0 = lo & ~31; c0 < hi || c0 == (lo & ~31); c0 += kPrepCols) {
-            const int n = max(0, min(kPrepCols, hi - c0));
+        // the first slots, on their way while the columns are cleared
+        int4 id0 = make_int4(-1, -1, -1, -1);
+        float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool first = vec && (int)threadIdx.x < a.K / 4;
+        if (first) {
+            id0 = __ldg(reinterpret_cast<const int4 *>(idx) + threadIdx.x);
+            v0 = __ldg(reinterpret_cast<const float4 *>(ds) + threadIdx.x);
+        }
+        for (int c0 = lo & ~31; c0 < hi || c0 == (lo & ~31); c0 += cols) {
+            const int n = max(0, min(cols, hi - c0));
             for (int j = threadIdx.x; j < n; j += kPrepThreads)
                 g[j] = 0.f;
             for (int j = threadIdx.x; j < (n + 31) / 32; j += kPrepThreads)
                 claimed[j] = 0u;
             __syncthreads();
             bool twice = false;
-            for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
-                const int id = __ldg(idx + k), j = id - c0;
+            auto slot = [&](int id, float v) {
+                const int j = id - c0;
                 if ((id < -1 || id >= a.P) && a.err)
                     atomicExch(a.err, kErrIndex);
                 if (id < lo || id >= hi || j < 0 || j >= n)
-                    continue;
+                    return;
                 if (atomicOr(&claimed[j >> 5], 1u << (j & 31)) & (1u << (j & 31)))
                     twice = true;
                 else
-                    g[j] = __ldg(ds + k);
+                    g[j] = v;
+            };
+            if (vec) {
+                if (first) {
+                    slot(id0.x, v0.x);
+                    slot(id0.y, v0.y);
+                    slot(id0.z, v0.z);
+                    slot(id0.w, v0.w);
+                }
+                for (int k = threadIdx.x + kPrepThreads; k < a.K / 4; k += kPrepThreads) {
+                    const int4 id = __ldg(reinterpret_cast<const int4 *>(idx) + k);
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(ds) + k);
+                    slot(id.x, v.x);
+                    slot(id.y, v.y);
+                    slot(id.z, v.z);
+                    slot(id.w, v.w);
+                }
+            } else {
+                for (int k = threadIdx.x; k < a.K; k += kPrepThreads) {
+                    const int id = __ldg(idx + k);
+                    const float v = __ldg(ds + k);
+                    slot(id, v);
+                }
             }
             if (__syncthreads_or(twice)) {
                 for (int j = threadIdx.x; j < n; j += kPrepThreads)
@@ -170,15 +203,30 @@ __global__ void __launch_bounds__(kPrepThreads)
                 }
                 __syncthreads();
             }
-            for (int j = threadIdx.x; j < n; j += kPrepThreads) {
-                const float v = g[j];
-                if (c0 + j >= lo)
-                    G[row * a.P + c0 + j] = v;
-                seen(v, c0 + j);
+            if (vec) {
+                // (whole quadruples: what lies past the candidates is written, not read)
+                for (int j = threadIdx.x * 4; j < n; j += kPrepThreads * 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(g + j);
+                    const float4 k4 = __ldg(reinterpret_cast<const float4 *>(ks + c0 + j));
+                    *reinterpret_cast<float4 *>(G + row * a.P + c0 + j) = v;
+                    const float vv[4] = {v.x, v.y, v.z, v.w}, kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < n)
+                            seen(vv[e], kk[e]);
+                }
+            } else {
+                for (int j = threadIdx.x; j < n; j += kPrepThreads) {
+                    const float v = g[j];
+                    if (c0 + j >= lo)
+                        G[row * a.P + c0 + j] = v;
+                    seen(v, __ldg(ks + c0 + j));
+                }
             }
             __syncthreads();
         }
     }
+    top[kMaxW] = finite(wv * qv);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         top[e] = __reduce_max_sync(0xffffffffu, top[e]);
@@ -934,49 +982,53 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     }
 }
 
-// dk: the partial sums of a pair's segments, added in the order of the shares
-// that made them. Thread = 4 values; a block stays within one pair's 256 keys.
+// dk: the partial sums of a pair's segments, added in a fixed order. One block a
+// key; the segments are cut into 1024 / D runs of neighbours, whose sums are
+// added in order, so that the loads of a long list are in flight together.
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p, int shares)
 {
-    const int per_row = a.D / 4, rows = 256 / per_row;       // keys a block
-    const int pair = (int)(blockIdx.x / per_row);            // 256 / rows = per_row blocks a pair
-    const int b = pair / p.n_pairs, kp = pair - b * p.n_pairs;
-    const int in = (int)(blockIdx.x - pair * per_row) * rows + threadIdx.x / per_row;
-    const int c = (threadIdx.x % per_row) * 4;
-    const int j = kp * 256 + in;
-    if (j >= a.P)
-        return;
+    __shared__ float4 run[256];
+    const int b = (int)(blockIdx.x / (unsigned)a.P), j = (int)(blockIdx.x - (unsigned)b * (unsigned)a.P);
+    const int kp = j >> 8, pair = b * p.n_pairs + kp;
+    const int per_row = a.D / 4, runs = 256 / per_row;
+    const int c = (threadIdx.x % per_row) * 4, me = threadIdx.x / per_row;
     int begin = p.per_seq * b;
     for (int k = 0; k < kp; ++k)
         begin += p.n_steps_seq - first_step(a, p, k);
     const int end = begin + p.n_steps_seq - first_step(a, p, kp);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (begin < end) {
-        // the share that holds step `begin`
+        // the shares that hold steps `begin` and `end - 1`
         const int longer = p.rest * (p.share + 1);
-        int x = begin < longer ? begin / (p.share + 1) : p.rest + (begin - longer) / p.share;
-        const float *src = p.part + ((int64_t)(x + pair) * 256 + in) * a.D + c;
-        int n = 0;
-        while (x + n < shares && share_start(p, x + n) < end)
-            ++n;
-        // eight loads in flight; the sums in the shares' order
-        for (int i = 0; i < n; i += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = i + e < n ? __ldcs(reinterpret_cast<const float4 *>(src + (int64_t)(i + e) * 256 * a.D))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s.x += v[e].x;
-                s.y += v[e].y;
-                s.z += v[e].z;
-                s.w += v[e].w;
-            }
+        auto share_of = [&](int at) {
+            return at < longer ? at / (p.share + 1) : p.rest + (at - longer) / p.share;
+        };
+        const int x0 = share_of(begin), n = share_of(end - 1) - x0 + 1;
+        const float *src = p.part + ((int64_t)(x0 + pair) * 256 + (j & 255)) * a.D + c;
+        const int per = (n + runs - 1) / runs;
+        const int i1 = min(n, (me + 1) * per);
+#pragma unroll 4
+        for (int i = me * per; i < i1; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)i * 256 * a.D);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
         }
     }
+    run[threadIdx.x] = s;
+    __syncthreads();
+    if (me)
+        return;
+    for (int i = 1; i < runs; ++i) {
+        const float4 v = run[i * per_row + threadIdx.x];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
     const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-    *reinterpret_cast<uint2 *>(a.dk + ((int64_t)b * a.P + j) * a.D + c) =
+    *reinterpret_cast<uint2 *>(a.dk + (int64_t)blockIdx.x * a.D + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
@@ -1000,7 +1052,7 @@ cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, 
     bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true, HP), st>>>(rows, keys, a, pq);
     if (grid_k > 0)
         bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false, HP), st>>>(keys, rows, a, pk);
-    bwd_reduce_kernel<<<(unsigned)(a.B * pk.n_pairs * (D / 4)), 256, 0, st>>>(a, pk, grid_k);
+    bwd_reduce_kernel<<<(unsigned)(a.B * a.P), 256, 0, st>>>(a, pk, grid_k);
     return cudaGetLastError();
 }
 
@@ -1078,7 +1130,10 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     cudaError_t e = cudaMemsetAsync(gmax, 0, kMaxWords * 4, stream);
     if (e != cudaSuccess)
         return e;
-    bwd_prep_kernel<<<a.B * a.S, kPrepThreads, 0, stream>>>(a, G, gmax, row_any);
+    // rows of idx, dscores, G and k_scale on 16-byte boundaries
+    const bool vec = a.idx && a.K % 4 == 0 && a.P % 4 == 0 && al16(a.idx) && al16(a.dscores) && al16(a.k_scale);
+    const int cols = a.idx ? (a.P < kPrepCols ? (a.P + 31) / 32 * 32 : kPrepCols) : 32;
+    bwd_prep_kernel<<<a.B * a.S, kPrepThreads, (size_t)cols * 4 + cols / 8, stream>>>(a, G, gmax, row_any, vec, cols);
     if (a.D == 32)
         return run_bwd_heads<32>(hp, a, pq, pk, grid_q, shares, stream);
     if (a.D == 64)

@@ -10,10 +10,14 @@
 //   codes 0, scale NaN), and is read back as code * scale.
 //
 // The codes are those of the formula in exact arithmetic. For 16-bit inputs
-// one correctly rounded division is enough: lim * x is exact in fp32, and a
+// one correctly rounded quotient is enough: lim * x is exact in fp32, and a
 // quotient of a 15- or 18-bit by an 11-bit integer that is no tie is further
 // from any tie than fp32's rounding. For fp32 inputs quotients next to a tie
-// are decided again in 64 bits.
+// are decided again in 64 bits. The quotient comes from the group's correctly
+// rounded reciprocal y by Markstein's theorem (IBM J. Res. Dev. 34, 1990): with
+// q0 = n y and the exact remainder r = n - d q0, q0 + r y is n / d correctly
+// rounded. Three instructions a value; a full division for each value bound
+// the kernel (52 us for 8 x 8192 rows of 512 against 15 us of HBM time).
 //
 // Bound: HBM (each value is read and each code written once); at a few rows,
 // the launch. One group is held by group/8 lanes, 8 values (one or two 16-byte
@@ -100,15 +104,19 @@ __device__ __forceinline__ float settle_tie(float v, float x, float amax)
     return nextafterf(tie, r > (double)tie ? INFINITY : -INFINITY);
 }
 
-// Two codes (low byte first) of two values of a group with maximum amax > 0.
+// Two codes (low byte first) of two values of a group with maximum d > 0 and
+// y = 1 / d, both in the middle of fp32's range.
 template <int CODE, bool TIES>
-__device__ __forceinline__ uint32_t codes2(float x0, float x1, float amax)
+__device__ __forceinline__ uint32_t codes2(float x0, float x1, float d, float y)
 {
     constexpr float lim = code_limit<CODE>();
-    float v0 = __fdiv_rn(lim * x0, amax), v1 = __fdiv_rn(lim * x1, amax);
+    const float n0 = lim * x0, n1 = lim * x1;
+    float v0 = n0 * y, v1 = n1 * y;
+    v0 = fmaf(fmaf(-d, v0, n0), y, v0);
+    v1 = fmaf(fmaf(-d, v1, n1), y, v1);
     if (TIES) {
-        v0 = settle_tie<CODE>(v0, x0, amax);
-        v1 = settle_tie<CODE>(v1, x1, amax);
+        v0 = settle_tie<CODE>(v0, x0, d);
+        v1 = settle_tie<CODE>(v1, x1, d);
     }
     if constexpr (CODE == 0)
         return (uint32_t)(__float2int_rn(v0) & 0xff) | ((uint32_t)(__float2int_rn(v1) & 0xff) << 8);
@@ -116,147 +124,231 @@ __device__ __forceinline__ uint32_t codes2(float x0, float x1, float amax)
         return __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The rows of one warp: lane l finds out where row l goes (or comes from), all of
+// them at once; the rows are then walked `RP = 32 / lanes of a row` at a time,
+// U such passes with their loads in flight together. (Found row by row, the
+// divisions by n and the page size cost more than the row.)
+struct RowWalk {
+    uint32_t n_rows;     // B n
+    int per_warp;        // rows of a warp, at most 32
+    int vecs;            // vectors of a row
+    int lane_log;        // lanes of a row, as a power of two
+};
+
 // LPG lanes hold one group of LPG * 8 * NCH values.
-template <class T, int CODE, bool VEC, int LPG, int NCH>
-__global__ void __launch_bounds__(kQ8Threads) q8_write_kernel(const Q8WriteArgs a, uint32_t groups_per_row,
-                                                              uint32_t n_units)
+template <class T, int CODE, bool VEC, int LPG, int NCH, int U>
+__global__ void __launch_bounds__(kQ8Threads) q8_write_kernel(const Q8WriteArgs a, const RowWalk w)
 {
-    const uint32_t unit = blockIdx.x * (kQ8Threads / LPG) + threadIdx.x / LPG;
-    const int l = threadIdx.x % LPG;
-    const uint32_t row = unit / groups_per_row;
-    const uint32_t gi = unit - row * groups_per_row;
-    int64_t dst = -1;
-    const T *src = nullptr;
-    if (unit < n_units) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = (blockIdx.x * (kQ8Threads / 32) + (threadIdx.x >> 5)) * (uint32_t)w.per_warp;
+    int64_t my_dst = -1, my_src = 0;
+    if (lane < w.per_warp && base + lane < w.n_rows) {
+        const uint32_t row = base + lane;
         const int b = (int)(row / (uint32_t)a.n);
         const int i = (int)(row - (uint32_t)b * (uint32_t)a.n);
         if (i < (a.n_new ? __ldg(a.n_new + b) : a.n)) {
-            const int64_t pos = (int64_t)(a.start ? __ldg(a.start + b) : 0) + i;
-            dst = page_row(a.map, b, pos);
-            if (dst < 0 && a.err && l == 0)
+            my_dst = page_row(a.map, b, (int64_t)(a.start ? __ldg(a.start + b) : 0) + i);
+            if (my_dst < 0 && a.err)
                 atomicExch(a.err, kErrIndex);
-            src = static_cast<const T *>(a.x) + (int64_t)b * a.stride_b + (int64_t)i * a.stride_n +
-                  (int64_t)gi * (LPG * 8 * NCH);
+            my_src = (int64_t)b * a.stride_b + (int64_t)i * a.stride_n;
         }
     }
-    float f[NCH][8];
-    uint32_t top = 0;    // |x| as bits: ordered as the values are, infinities and NaN above every number
+    const int RP = 32 >> w.lane_log, l = lane & ((1 << w.lane_log) - 1), gpr = a.D / a.group;
+    for (int r0 = 0; r0 < w.per_warp; r0 += U * RP) {
+        int64_t dst[U], src[U];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        if (dst >= 0) {
-            load8<T, VEC>(src + c * (LPG * 8) + l * 8, f[c]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[c][i] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * RP + (lane >> w.lane_log);
+            dst[u] = __shfl_sync(0xffffffffu, my_dst, r & 31);
+            src[u] = __shfl_sync(0xffffffffu, my_src, r & 31);
+            if (r >= w.per_warp)
+                dst[u] = -1;
         }
+        for (int v0 = 0; v0 < w.vecs; v0 += 32 * NCH) {
+            float f[U][NCH][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            top = max(top, __float_as_uint(f[c][i]) & 0x7fffffffu);
-    }
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int o = LPG / 2; o >= 1; o >>= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (dst < 0)
-        return;
-    const bool finite = top < 0x7f800000u;
-    const float amax = __uint_as_float(top);
-    // lim * x must not pass fp32's range: large groups are scaled down exactly
-    const float shrink = (sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value) || amax < 0x1p118f ? 1.f : 0x1p-16f;
-    const float den = amax * shrink;
-    uint8_t *out = a.cache + dst * a.D + (int64_t)gi * (LPG * 8 * NCH);
+                for (int c = 0; c < NCH; ++c) {
+                    const int v = v0 + c * 32 + l;
+                    if (dst[u] >= 0 && v < w.vecs) {
+                        load8<T, VEC>(static_cast<const T *>(a.x) + src[u] + v * 8, f[u][c]);
+                    } else {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        uint32_t w[2] = {0u, 0u};
-        if (finite && top != 0u) {
+                        for (int i = 0; i < 8; ++i)
+                            f[u][c][i] = 0.f;
+                    }
+                }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i >> 1] |= codes2<CODE, sizeof(T) == 4>(f[c][2 * i] * shrink, f[c][2 * i + 1] * shrink, den)
-                             << (16 * (i & 1));
+            for (int u = 0; u < U; ++u) {
+                uint32_t top = 0;    // |x| as bits: ordered as the values are, infinities and NaN above every number
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        top = max(top, __float_as_uint(f[u][c][i]) & 0x7fffffffu);
+#pragma unroll
+                for (int o = LPG / 2; o >= 1; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (dst[u] < 0 || v0 + l >= w.vecs)
+                    continue;
+                const bool finite = top < 0x7f800000u;
+                const float amax = __uint_as_float(top);
+                // Very large and very small groups are moved, exactly, to where neither
+                // lim * x nor the remainders of quotients that matter (codes 2^-10 up) leave
+                // fp32's normal range; values that become subnormal on the way have code 0.
+                const float shift = amax >= 0x1p60f ? 0x1p-64f : (amax < 0x1p-60f ? 0x1p64f : 1.f);
+                const float den = amax * shift;
+                const float inv = __frcp_rn(den);
+                uint8_t *out = a.cache + dst[u] * a.D;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    uint32_t q[2] = {0u, 0u};
+                    if (finite && top != 0u) {
+                        if (shift != 1.f) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                f[u][c][i] *= shift;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            q[i >> 1] |= codes2<CODE, sizeof(T) == 4>(f[u][c][2 * i], f[u][c][2 * i + 1], den, inv)
+                                         << (16 * (i & 1));
+                    }
+                    *reinterpret_cast<uint2 *>(out + (v0 + c * 32 + l) * 8) = make_uint2(q[0], q[1]);
+                }
+                if ((l & (LPG - 1)) == 0)
+                    a.scales[dst[u] * gpr + (v0 + l) / (LPG * NCH)] =
+                        finite ? __fdiv_rn(amax, code_limit<CODE>()) : __int_as_float(0x7fc00000);
+            }
         }
-        *reinterpret_cast<uint2 *>(out + c * (LPG * 8) + l * 8) = make_uint2(w[0], w[1]);
     }
-    if (l == 0)
-        a.scales[dst * groups_per_row + gi] =
-            finite ? __fdiv_rn(amax, code_limit<CODE>()) : __int_as_float(0x7fc00000);
 }
 
-// Sixteen codes a thread: one 16-byte load, two (fp32: four) 16-byte stores.
-template <class T, int CODE>
-__global__ void __launch_bounds__(kQ8Threads) q8_read_kernel(const Q8ReadArgs a, uint32_t parts_per_row,
-                                                             uint64_t n_parts)
+// Sixteen codes a lane: one 16-byte load, two (fp32: four) 16-byte stores.
+template <class T, int CODE, int U>
+__global__ void __launch_bounds__(kQ8Threads) q8_read_kernel(const Q8ReadArgs a, const RowWalk w)
 {
-    const uint64_t part = (uint64_t)blockIdx.x * kQ8Threads + threadIdx.x;
-    if (part >= n_parts)
-        return;
-    const uint32_t row = (uint32_t)(part / parts_per_row);
-    const uint32_t p = (uint32_t)(part - (uint64_t)row * parts_per_row);
-    const int b = (int)(row / (uint32_t)a.n);
-    const int i = (int)(row - (uint32_t)b * (uint32_t)a.n);
-    int64_t pos;
-    bool want = true, bad = false;
-    if (a.idx) {
-        pos = __ldg(a.idx + row);
-        want = pos != -1;
-        bad = pos < -1;
-    } else {
-        pos = (int64_t)(a.start ? __ldg(a.start + b) : 0) + i;
-        bad = pos < 0;
-    }
-    if (want && !bad && a.lens)
-        want = pos < __ldg(a.lens + b);
-    int64_t src = -1;
-    if (want && !bad) {
-        src = page_row(a.map, b, pos);
-        bad = src < 0;
-    }
-    if (bad && a.err)
-        atomicExch(a.err, kErrIndex);
-    alignas(16) T o[16];
-    if (src >= 0) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(a.cache + src * a.D) + p);
-        const float sc = __ldg(a.scales + src * (a.D / a.group) + (p * 16u) / (uint32_t)a.group);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t two = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-            float c0, c1;
-            if constexpr (CODE == 0) {
-                c0 = (float)(int8_t)(two & 0xffu);
-                c1 = (float)(int8_t)(two >> 8);
-            } else {
-                const __half2 h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-                c0 = __low2float(h);
-                c1 = __high2float(h);
-            }
-            o[2 * e] = from_f32<T>(c0 * sc);
-            o[2 * e + 1] = from_f32<T>(c1 * sc);
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = (blockIdx.x * (kQ8Threads / 32) + (threadIdx.x >> 5)) * (uint32_t)w.per_warp;
+    int64_t my_src = -1;
+    if (lane < w.per_warp && base + lane < w.n_rows) {
+        const uint32_t row = base + lane;
+        const int b = (int)(row / (uint32_t)a.n);
+        const int i = (int)(row - (uint32_t)b * (uint32_t)a.n);
+        int64_t pos;
+        bool want = true, bad = false;
+        if (a.idx) {
+            pos = __ldg(a.idx + row);
+            want = pos != -1;
+            bad = pos < -1;
+        } else {
+            pos = (int64_t)(a.start ? __ldg(a.start + b) : 0) + i;
+            bad = pos < 0;
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            o[e] = from_f32<T>(0.f);
+        if (want && !bad && a.lens)
+            want = pos < __ldg(a.lens + b);
+        if (want && !bad) {
+            my_src = page_row(a.map, b, pos);
+            bad = my_src < 0;
+        }
+        if (bad && a.err)
+            atomicExch(a.err, kErrIndex);
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + (int64_t)row * a.D + p * 16);
+    const int RP = 32 >> w.lane_log, l = lane & ((1 << w.lane_log) - 1), gpr = a.D / a.group;
+    for (int r0 = 0; r0 < w.per_warp; r0 += U * RP) {
+        int64_t src[U];
+        bool live[U];
 #pragma unroll
-    for (int e = 0; e < (int)sizeof(T); ++e)
-        dst[e] = reinterpret_cast<const uint4 *>(o)[e];
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * RP + (lane >> w.lane_log);
+            src[u] = __shfl_sync(0xffffffffu, my_src, r & 31);
+            live[u] = r < w.per_warp && base + r < w.n_rows;
+        }
+        for (int v = l; v < w.vecs; v += 32) {
+            uint4 q[U];
+            float sc[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                q[u] = make_uint4(0u, 0u, 0u, 0u);      // code 0 and scale 0: a row of zeros
+                sc[u] = 0.f;
+                if (live[u] && src[u] >= 0) {
+                    q[u] = __ldg(reinterpret_cast<const uint4 *>(a.cache + src[u] * a.D) + v);
+                    sc[u] = __ldg(a.scales + src[u] * gpr + (uint32_t)v * 16u / (uint32_t)a.group);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!live[u])
+                    continue;
+                alignas(16) T o[16];
+                const uint32_t c[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t two = (c[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                    float c0, c1;
+                    if constexpr (CODE == 0) {
+                        c0 = (float)(int8_t)(two & 0xffu);
+                        c1 = (float)(int8_t)(two >> 8);
+                    } else {
+                        const __half2 h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+                        c0 = __low2float(h);
+                        c1 = __high2float(h);
+                    }
+                    o[2 * e] = from_f32<T>(c0 * sc[u]);
+                    o[2 * e + 1] = from_f32<T>(c1 * sc[u]);
+                }
+                const int64_t row = (int64_t)base + r0 + u * RP + (lane >> w.lane_log);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * a.D + v * 16);
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(T); ++e)
+                    dst[e] = reinterpret_cast<const uint4 *>(o)[e];
+            }
+        }
+    }
+}
+
+// Rows of `vecs` vectors. Few rows: one pass a warp, for the latency; where
+// that still gives 32 warps an SM, four passes a warp, two at a time.
+RowWalk plan_rows(int64_t n_rows, int vecs, bool &deep, unsigned &blocks)
+{
+    RowWalk w;
+    w.n_rows = (uint32_t)n_rows;
+    w.vecs = vecs;
+    w.lane_log = 0;
+    while (w.lane_log < 5 && (1 << w.lane_log) < vecs)
+        ++w.lane_log;
+    const int rp = 32 >> w.lane_log;
+    deep = rp <= 8 && n_rows / (4 * rp) >= 148 * 32;
+    w.per_warp = deep ? 4 * rp : rp;
+    const int64_t per_block = (int64_t)w.per_warp * (kQ8Threads / 32);
+    blocks = (unsigned)((n_rows + per_block - 1) / per_block);
+    return w;
+}
+
+template <class T, int CODE, bool VEC, int LPG, int NCH>
+cudaError_t run_write(const Q8WriteArgs &a, cudaStream_t st)
+{
+    bool deep;
+    unsigned blocks;
+    const RowWalk w = plan_rows((int64_t)a.B * a.n, a.D / 8, deep, blocks);
+    if (deep)
+        q8_write_kernel<T, CODE, VEC, LPG, NCH, 2><<<blocks, kQ8Threads, 0, st>>>(a, w);
+    else
+        q8_write_kernel<T, CODE, VEC, LPG, NCH, 1><<<blocks, kQ8Threads, 0, st>>>(a, w);
+    return cudaGetLastError();
 }
 
 template <class T, int CODE, bool VEC>
 cudaError_t write_group(const Q8WriteArgs &a, cudaStream_t st)
 {
-    const uint32_t gpr = (uint32_t)(a.D / a.group);
-    const uint32_t units = (uint32_t)a.B * (uint32_t)a.n * gpr;
-    auto blocks = [&](int lpg) { return (unsigned)(((uint64_t)units * lpg + kQ8Threads - 1) / kQ8Threads); };
     switch (a.group) {
-    case 32: q8_write_kernel<T, CODE, VEC, 4, 1><<<blocks(4), kQ8Threads, 0, st>>>(a, gpr, units); break;
-    case 64: q8_write_kernel<T, CODE, VEC, 8, 1><<<blocks(8), kQ8Threads, 0, st>>>(a, gpr, units); break;
-    case 128: q8_write_kernel<T, CODE, VEC, 16, 1><<<blocks(16), kQ8Threads, 0, st>>>(a, gpr, units); break;
-    case 256: q8_write_kernel<T, CODE, VEC, 32, 1><<<blocks(32), kQ8Threads, 0, st>>>(a, gpr, units); break;
-    default: q8_write_kernel<T, CODE, VEC, 32, 2><<<blocks(32), kQ8Threads, 0, st>>>(a, gpr, units); break;
+    case 32: return run_write<T, CODE, VEC, 4, 1>(a, st);
+    case 64: return run_write<T, CODE, VEC, 8, 1>(a, st);
+    case 128: return run_write<T, CODE, VEC, 16, 1>(a, st);
+    case 256: return run_write<T, CODE, VEC, 32, 1>(a, st);
+    default: return run_write<T, CODE, VEC, 32, 2>(a, st);
     }
-    return cudaGetLastError();
 }
 
 template <class T>
@@ -272,13 +364,20 @@ cudaError_t write_type(const Q8WriteArgs &a, int code, cudaStream_t st)
 template <class T>
 cudaError_t read_type(const Q8ReadArgs &a, int code, cudaStream_t st)
 {
-    const uint32_t ppr = (uint32_t)(a.D / 16);
-    const uint64_t parts = (uint64_t)a.B * (uint64_t)a.n * ppr;
-    const unsigned blocks = (unsigned)((parts + kQ8Threads - 1) / kQ8Threads);
-    if (code == 0)
-        q8_read_kernel<T, 0><<<blocks, kQ8Threads, 0, st>>>(a, ppr, parts);
-    else
-        q8_read_kernel<T, 1><<<blocks, kQ8Threads, 0, st>>>(a, ppr, parts);
+    bool deep;
+    unsigned blocks;
+    const RowWalk w = plan_rows((int64_t)a.B * a.n, a.D / 16, deep, blocks);
+    if (code == 0) {
+        if (deep)
+            q8_read_kernel<T, 0, 2><<<blocks, kQ8Threads, 0, st>>>(a, w);
+        else
+            q8_read_kernel<T, 0, 1><<<blocks, kQ8Threads, 0, st>>>(a, w);
+    } else {
+        if (deep)
+            q8_read_kernel<T, 1, 2><<<blocks, kQ8Threads, 0, st>>>(a, w);
+        else
+            q8_read_kernel<T, 1, 1><<<blocks, kQ8Threads, 0, st>>>(a, w);
+    }
     return cudaGetLastError();
 }
 
