@@ -42,8 +42,6 @@ template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <>
 __device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
 
 template <class T>
 __device__ __forceinline__ T from_f32(float x);
@@ -54,24 +52,77 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 
+// Eight values as they lie in memory.
+template <class T>
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+
 // Eight values starting at p: 16-byte loads when the rows allow them (VEC),
 // element loads otherwise.
 template <class T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, float (&f)[8])
+__device__ __forceinline__ Raw<T> load8(const T *p)
 {
-    alignas(16) T t[8];
+    Raw<T> r;
     if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<uint4 *>(t)[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    } else {
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            t[i] = p[i];
-    }
+            r.w[i] = __float_as_uint(p[i]);
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = to_f32<T>(t[i]);
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+    }
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ float value(const Raw<T> &r, int i)
+{
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(r.w[i]);
+    } else {
+        const uint16_t h = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+        return to_f32<T>(*reinterpret_cast<const T *>(&h));
+    }
+}
+
+// The largest magnitude of the eight, as the type's bits (ordered as the values
+// are, infinities and NaN above every number); and such bits as an fp32 number.
+template <class T>
+__device__ __forceinline__ uint32_t top_bits(const Raw<T> &r)
+{
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = max(m, r.w[i] & 0x7fffffffu);
+        return m;
+    } else {
+        constexpr uint32_t abs2 = 0x7fff7fffu;
+        const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(r.w[0] & abs2, r.w[1] & abs2, r.w[2] & abs2), r.w[3] & abs2, 0u);
+        return max(m & 0xffffu, m >> 16);
+    }
+}
+template <class T>
+__device__ __forceinline__ float from_bits(uint32_t b)
+{
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(b);
+    } else {
+        const uint16_t h = (uint16_t)b;
+        return to_f32<T>(*reinterpret_cast<const T *>(&h));
+    }
 }
 
 template <int CODE>
@@ -124,6 +175,18 @@ __device__ __forceinline__ uint32_t codes2(float x0, float x1, float d, float y)
         return __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
 }
 
+// amax / lim, correctly rounded (the same theorem; below 2^-90, where a remainder
+// may be subnormal, by a division).
+template <int CODE>
+__device__ __forceinline__ float scale_of(float amax)
+{
+    constexpr float lim = code_limit<CODE>(), y = 1.f / lim;
+    if (amax < 0x1p-90f)
+        return __fdiv_rn(amax, lim);
+    const float q = amax * y;
+    return fmaf(fmaf(-lim, q, amax), y, q);
+}
+
 // The rows of one warp: lane l finds out where row l goes (or comes from), all of
 // them at once; the rows are then walked `RP = 32 / lanes of a row` at a time,
 // U such passes with their loads in flight together. (Found row by row, the
@@ -165,35 +228,31 @@ __global__ void __launch_bounds__(kQ8Threads) q8_write_kernel(const Q8WriteArgs 
                 dst[u] = -1;
         }
         for (int v0 = 0; v0 < w.vecs; v0 += 32 * NCH) {
-            float f[U][NCH][8];
+            Raw<T> f[U][NCH];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
                     const int v = v0 + c * 32 + l;
                     if (dst[u] >= 0 && v < w.vecs) {
-                        load8<T, VEC>(static_cast<const T *>(a.x) + src[u] + v * 8, f[u][c]);
+                        f[u][c] = load8<T, VEC>(static_cast<const T *>(a.x) + src[u] + v * 8);
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            f[u][c][i] = 0.f;
+                        f[u][c] = Raw<T>{};
                     }
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t top = 0;    // |x| as bits: ordered as the values are, infinities and NaN above every number
+                uint32_t top = 0;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        top = max(top, __float_as_uint(f[u][c][i]) & 0x7fffffffu);
+                    top = max(top, top_bits<T>(f[u][c]));
 #pragma unroll
                 for (int o = LPG / 2; o >= 1; o >>= 1)
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                 if (dst[u] < 0 || v0 + l >= w.vecs)
                     continue;
-                const bool finite = top < 0x7f800000u;
-                const float amax = __uint_as_float(top);
+                const float amax = from_bits<T>(top);
+                const bool finite = __float_as_uint(amax) < 0x7f800000u;
                 // Very large and very small groups are moved, exactly, to where neither
                 // lim * x nor the remainders of quotients that matter (codes 2^-10 up) leave
                 // fp32's normal range; values that become subnormal on the way have code 0.
@@ -205,21 +264,17 @@ __global__ void __launch_bounds__(kQ8Threads) q8_write_kernel(const Q8WriteArgs 
                 for (int c = 0; c < NCH; ++c) {
                     uint32_t q[2] = {0u, 0u};
                     if (finite && top != 0u) {
-                        if (shift != 1.f) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                f[u][c][i] *= shift;
-                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            q[i >> 1] |= codes2<CODE, sizeof(T) == 4>(f[u][c][2 * i], f[u][c][2 * i + 1], den, inv)
+                            q[i >> 1] |= codes2<CODE, sizeof(T) == 4>(value(f[u][c], 2 * i) * shift,
+                                                                      value(f[u][c], 2 * i + 1) * shift, den, inv)
                                          << (16 * (i & 1));
                     }
                     *reinterpret_cast<uint2 *>(out + (v0 + c * 32 + l) * 8) = make_uint2(q[0], q[1]);
                 }
                 if ((l & (LPG - 1)) == 0)
                     a.scales[dst[u] * gpr + (v0 + l) / (LPG * NCH)] =
-                        finite ? __fdiv_rn(amax, code_limit<CODE>()) : __int_as_float(0x7fc00000);
+                        finite ? scale_of<CODE>(amax) : __int_as_float(0x7fc00000);
             }
         }
     }
