@@ -135,11 +135,16 @@ def version() -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream of a device as its handle (a Stream object costs as much
+# as a small launch).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream(dev: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(dev.index)
 
 
 def _check(st: int, where: str):
