@@ -339,7 +339,7 @@ struct BwSmem {
     uint64_t c_empty[2];                 // fp16 tiles read
     uint64_t s_full[2][2];               // per stationary tile and half: products there
     uint64_t m_full[2][2][2];            // per tile and half, even and odd steps: M and B2 there
-    uint64_t acc_full[2];
+    uint64_t acc_full[2], acc_empty[2];  // per tile: an item's accumulator there; read by both halves
     uint64_t g_full[2], g_empty[2];      // dq: gk staged, read
     uint64_t dw_full[2];                 // dq, per tile: the second half's part of dw
     float dw[2][128];
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 mbar_init(&sm->m_full[i][h][1], 4 + kConv);
             }
             mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->acc_empty[i], 8);
             mbar_init(&sm->g_full[i], 4);
             mbar_init(&sm->g_empty[i], 16);
             mbar_init(&sm->dw_full[i], 4);
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         const uint64_t b_desc = sdesc_k_rows<D>(smem_u32(sb));
         const uint64_t c_desc = sdesc_mn_rows<kC>(smem_u32(sc), 128 * kC);
         const uint32_t t_s = tmem + i * 128, t_acc = tmem + 256 + i * D;
-        int stage = 0, item = -1, n = 0;
+        int stage = 0, item = -1, n = 0, items = 0;
         uint32_t phase = 0;
         bool issued = false;
         // S = A B^T of the walk's step, for the 64 rows of B that half `hf` names
@@ -550,6 +551,12 @@ __global__ void __launch_bounds__(kBwThreads, 1)
 #pragma unroll
             for (int hf = 0; hf < 2 && ok; ++hf) {
                 ok = warp_mbar_wait_short(&sm->m_full[i][hf][n & 1], (n >> 1) & 1, abort_flag, a.err);
+                // an item's first products overwrite the accumulator: the last item's must
+                // have been read (the first half is there before the second has read it)
+                if (ok && hf == 0 && fresh) {
+                    ok = warp_mbar_wait_short(&sm->acc_empty[i], (items & 1) ^ 1u, abort_flag, a.err);
+                    ++items;
+                }
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -746,15 +753,18 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             bool any = false, old_any = false, pending = false;
             uint64_t dw[2] = {0u, 0u};                  // two fp32 sums each
             auto finish = [&]() -> bool {
+                if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
+                    return false;
+                // (the item's accumulator is complete only after the first half has been
+                // through its previous finish(): its word of that item has been read)
                 if (half) {
                     sm->dw[i][r] = old_dw;
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&sm->dw_full[i]);
-                }
-                if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err) ||
-                    (!half && !warp_mbar_wait_short(&sm->dw_full[i], items & 1, abort_flag, a.err)))
+                } else if (!warp_mbar_wait_short(&sm->dw_full[i], items & 1, abort_flag, a.err)) {
                     return false;
+                }
                 ++items;
                 pending = false;
                 tc_fence_after();
@@ -793,6 +803,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                             *reinterpret_cast<uint4 *>(a.dq + (int64_t)dst[e] * D + half * (D / 2) + c + u * 8) = o;
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm->acc_empty[i]);
                 return true;
             };
             bool go = wk.begin(a, p), ok = true;
@@ -969,6 +983,9 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                                             __uint_as_float(v[e + 3]) * inv * inv_w);
                     }
                     tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm->acc_empty[i]);
                 }
             }
         }

@@ -340,3 +340,23 @@ def test_many_slots_of_one_block(sai):
     again = sai.indexer_scores_backward(*a, cr, t_begin=20000)
     for x, y in zip(got, again):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("S,H,D,cr,K", [(1500, 64, 64, 4, 60), (2600, 128, 32, 8, 0), (1400, 64, 32, 2, 100)])
+def test_many_tiles_a_block_of_threads(sai, S, H, D, cr, K):
+    """More token tiles than the GPU has SMs, from one key tile to several each:
+    every SM works through a list of them, its last ones the shortest. Twenty
+    runs give the same bits, and they are the formula's."""
+    B, P = 1, S // cr
+    q8, qs, w, k8, ks = inputs(S, B, S, H, D, P)
+    mask = ref.candidates(B, S, P, cr)
+    if K:
+        idx, ds = selection(S, mask, K)
+    else:
+        idx, ds = None, (np.random.default_rng(S).standard_normal((B, S, P)) * 1e-5).astype(np.float32)
+    a = dev(ds, idx, q8, qs, w, k8, ks)
+    first = sai.indexer_scores_backward(*a, cr)
+    check(first, ref.dense(ds, idx, mask), q8, qs, w, k8, ks)
+    for _ in range(20):
+        for x, y in zip(sai.indexer_scores_backward(*a, cr), first):
+            assert torch.equal(x, y)
