@@ -27,8 +27,8 @@
 //
 // One CTA per SM walks work items (sequence, TT tokens, a range of key tiles).
 // Warp roles (384 threads): warp 0 brings key tiles into a ring (TMA; a tile of
-// a paged cache page by page) with their scales (cp.async, completing on the
-// same barrier), warp 1 issues the MMAs, warps 2 and 3 prepare alternate items
+// a paged cache page by page) with their scales (bulk copies, or cp.async where
+// rows have no 16-byte boundary, completing on the same barrier), warp 1 issues the MMAs, warps 2 and 3 prepare alternate items
 // ahead of the others (bounds, query tile by TMA, the columns' weights) and
 // fill their outputs that have no candidate with -inf, warps 4..7 and 8..11 are
 // two epilogue groups taking alternate tiles, each with its own 256-column
@@ -61,6 +61,7 @@ struct ScPlan {
     int groups;         // epilogue groups a tile (128 columns each)
     int box_rows;       // rows of a key load
     int loads;          // loads a key tile
+    int bulk;           // scales come in whole 16-byte pieces (else word by word)
 };
 
 // One item: TT tokens of a sequence and the key tiles [c_lo, c_hi); those in
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             mbar_init(&sm->i_empty[i], kScItemReaders);
         }
         for (int s = 0; s < kScRing; ++s) {
-            mbar_init(&sm->k_full[s], 1 + 32);      // the tile's bytes, each lane's scales
+            mbar_init(&sm->k_full[s], p.bulk ? 1 : 1 + 32);   // the tile's bytes; each lane's scales
             mbar_init(&sm->k_empty[s], 4 * p.groups);  // the tile's epilogue warps: its products are done then
         }
         for (int i = 0; i < 4; ++i) {
@@ -205,26 +206,26 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     ok = false;
                     break;
                 }
+                const float *first = a.k_scale + (int64_t)page * a.map.page + row;   // scale of this load's first row
+                uint32_t bytes = page >= 0 ? (uint32_t)(p.box_rows * D) : 0u, sbytes = 0;
+                if (p.bulk && page >= 0)
+                    sbytes = (uint32_t)min(p.box_rows, a.map.page - row) * 4u;
+                const uint32_t total = __reduce_add_sync(0xffffffffu, bytes + sbytes);
                 if (lane == 0) {
                     sm->have[stage] = have;
-                    mbar_arrive_expect_tx(&sm->k_full[stage], (uint32_t)(__popc(have) * p.box_rows * D));
+                    mbar_arrive_expect_tx(&sm->k_full[stage], total);
                 }
                 __syncwarp();
-                if (page >= 0)
+                if (page >= 0) {
                     tma_load_3d(sk + stage * k_bytes + lane * p.box_rows * D, &mapK, &sm->k_full[stage], 0, row,
                                 page);
+                    if (p.bulk)
+                        bulk_load(smem_u32(&sm->ks[stage][lane * p.box_rows]), first, sbytes, &sm->k_full[stage]);
+                }
                 __syncwarp();
-                const float *first = a.k_scale + (int64_t)page * a.map.page + row;   // scale of this load's first row
-                const uint32_t to = smem_u32(&sm->ks[stage][lane]);
-                const int left = n_keys - k * 128;
-                if (p.loads == 1) {
-                    const float *f = reinterpret_cast<const float *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(first), 0)) + lane;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (have && i * 32 + lane < left)
-                            cp_async4(to + i * 128, f + i * 32);
-                } else {
+                if (!p.bulk) {
+                    const uint32_t to = smem_u32(&sm->ks[stage][lane]);
+                    const int left = n_keys - k * 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float *f = reinterpret_cast<const float *>(
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         if (((have >> from[i]) & 1u) && i * 32 + lane < left)
                             cp_async4(to + i * 128, f + off[i]);
                     }
+                    cp_async_arrive(&sm->k_full[stage]);
                 }
-                cp_async_arrive(&sm->k_full[stage]);
                 k_used |= 1u << stage;
                 k_parity = (k_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == kScRing) {
@@ -617,6 +618,7 @@ cudaError_t launch_indexer_scores(const ScoresArgs &a, cudaStream_t stream)
     p.box_rows = a.map.page < 128 ? a.map.page : 128;
     p.loads = a.map.max_pages > 1 && a.map.page < 128 ? 128 / a.map.page : 1;
     p.groups = p.tt * hp > 128 ? 2 : 1;
+    p.bulk = a.map.page % 4 == 0 && al16(a.k_scale) ? 1 : 0;
     CUtensorMap mq, mk;
     if (!make_map_q8(&mq, a.q8, a.D, a.H, (uint64_t)a.B * a.S, hp, p.tt) ||
         !make_map_q8(&mk, a.cache, a.D, a.map.page, a.map.n_pages, p.box_rows, 1))

@@ -199,6 +199,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses on 16-byte
+// boundaries) from global memory to smem, counted on the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_smem),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // 16-byte global -> smem copy through L2 (LSU path, not cached in L1).
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void *src)
 {
