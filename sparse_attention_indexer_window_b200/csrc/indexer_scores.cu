@@ -181,26 +181,39 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 slot = 0;
                 iphase ^= 1u;
             }
-            // a tile's pages, one a lane (one load a lane), found one tile ahead
-            int next = -1, next_row = 0;
-            auto find = [&](int k) {
-                next = -1;
-                const int j0 = k * 128 + lane * p.box_rows;
-                if (k >= k_hi || lane >= p.loads || j0 >= n_keys)
+            // The pages of 32 / loads tiles at a time, one a lane, read from the table a
+            // batch ahead (read tile by tile, the table's latency bound a paged walk)
+            const int per = 32 / p.loads, sub = lane % p.loads;
+            int ahead = -1, ahead_row = 0, batch = -1, batch_row = 0;
+            auto find = [&](int kb) {
+                const int k = kb + lane / p.loads, j0 = k * 128 + sub * p.box_rows;
+                ahead = -1;
+                ahead_row = 0;
+                if (k >= k_hi || j0 >= n_keys || lane >= per * p.loads)
                     return;
-                next = b;
-                next_row = j0;
+                ahead = b;
+                ahead_row = j0;
                 if (a.map.table) {
                     const uint32_t pi = (uint32_t)j0 / (uint32_t)a.map.page;
-                    next_row = j0 - (int)pi * a.map.page;
-                    next = __ldg(a.map.table + (int64_t)b * a.map.max_pages + pi);
+                    ahead_row = j0 - (int)pi * a.map.page;
+                    ahead = __ldg(a.map.table + (int64_t)b * a.map.max_pages + pi);
                 }
             };
             find(k_lo);
+            int in = per;                             // tile within the batch
             for (int k = k_lo; k < k_hi; ++k) {
-                const int page = next >= 0 && next < a.map.n_pages ? next : -1;   // the epilogue reports the others
-                const int row = next_row;
-                find(k + 1);
+                if (in == per) {
+                    batch = ahead;
+                    batch_row = ahead_row;
+                    find(k + per);
+                    in = 0;
+                }
+                const int at = in * p.loads + (lane < p.loads ? lane : 0);
+                int page = __shfl_sync(0xffffffffu, batch, at);
+                const int row = __shfl_sync(0xffffffffu, batch_row, at);
+                ++in;
+                if (lane >= p.loads || page >= a.map.n_pages)     // the epilogue reports pages outside the cache
+                    page = -1;
                 const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
                 if (!warp_mbar_wait_short(&sm->k_empty[stage], phase ^ 1u, abort_flag, a.err)) {
                     ok = false;
