@@ -627,8 +627,10 @@ sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const floa
  *
  * the gradients with respect to the values that the codes stand for (rounding
  * to codes passes a gradient on as it is). An entry with G = 0 contributes
- * nothing, whatever its scale holds. Deterministic: the same inputs give the
- * same bits.
+ * nothing, whatever its scale holds; a token with no other entry has zero
+ * gradients, whatever its weights hold. (A NaN or infinite weight of a token
+ * that has a gradient makes dk NaN, for every key of its sequence.)
+ * Deterministic: the same inputs give the same bits.
  *
  *   dscores  [B,S,K] fp32 (sai_distill_kl's); idx [B,S,K] int32, or NULL
  *            (K = P); an entry outside {-1} U [0,P) is ignored and sets
