@@ -141,6 +141,7 @@ def _ptr(t: Optional[torch.Tensor]):
 # The current stream of a device as its handle (a Stream object costs as much
 # as a small launch).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream(dev: torch.device):
@@ -157,7 +158,7 @@ def _call(fn, dev: torch.device, *args) -> int:
     takes its device (SM count, TMA encoding, the allocation-free call's
     scratch array) from the current device, and the stream passed is that
     device's current stream."""
-    if dev.index == torch.cuda.current_device():   # (switching and back costs more than a small launch)
+    if dev.index == _current_device():   # (switching and back costs more than a small launch)
         return fn(*args, _stream(dev))
     with torch.cuda.device(dev):
         return fn(*args, _stream(dev))
@@ -544,33 +545,54 @@ def _on(dev: torch.device, **tensors):
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
+def _need(t: torch.Tensor, name: str, dtype, shape, dev: torch.device) -> int:
+    """The pointer of a contiguous tensor of this type and shape on dev (at a
+    few rows these checks are most of a call's time, so a tensor that passes is
+    asked four things and no more; one that does not gets the reason)."""
+    if t.dtype == dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, name, dtype, shape)
+    _on(dev, **{name: t})
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype, shape, dev: torch.device) -> Optional[int]:
+    return None if t is None else _need(t, name, dtype, shape, dev)
+
+
+def _err(t: Optional[torch.Tensor], dev: torch.device) -> Optional[int]:
+    return None if t is None else _need(t, "err", torch.int32, t.shape, dev)
+
+
 def _row_type(dtype, name: str) -> int:
     if dtype not in _ROW_TYPES:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
     return _ROW_TYPES[dtype]
 
 
-def _cache_args(cache: torch.Tensor, scales: torch.Tensor, block_table: Optional[torch.Tensor], B: int):
-    """(code, n_pages, page, D, group, max_pages) of a checked cache."""
+def _cache_args(cache: torch.Tensor, scales: torch.Tensor, block_table: Optional[torch.Tensor], B: int,
+                dev: torch.device):
+    """(code, n_pages, page, D, group, max_pages) of a checked cache and the
+    pointers of its three tensors."""
     if cache.dtype not in _CODES:
         raise TypeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
     if cache.dim() != 3:
         raise ValueError(f"cache must be [n_pages,page,D], got {tuple(cache.shape)}")
     n_pages, page, D = cache.shape
-    _want(cache, "cache", cache.dtype)
-    if scales.dim() != 3 or tuple(scales.shape[:2]) != (n_pages, page) or D == 0 or scales.shape[2] == 0 \
-            or D % scales.shape[2]:
+    G = scales.shape[2] if scales.dim() == 3 else 0
+    if G == 0 or D == 0 or D % G or scales.shape != (n_pages, page, G):
         raise ValueError(f"scales must be [n_pages,page,D/group] beside a cache of {tuple(cache.shape)}, "
                          f"got {tuple(scales.shape)}")
-    _want(scales, "scales", torch.float32)
     if block_table is None:
-        max_pages = 1
+        max_pages, tp = 1, None
     else:
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"block_table must be [B,max_pages] with B = {B}, got {tuple(block_table.shape)}")
-        _want(block_table, "block_table", torch.int32)
         max_pages = block_table.shape[1]
-    return _CODES[cache.dtype], n_pages, page, D, D // scales.shape[2], max_pages
+        tp = _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    return (_CODES[cache.dtype], n_pages, page, D, D // G, max_pages,
+            _need(cache, "cache", cache.dtype, (n_pages, page, D), dev),
+            _need(scales, "scales", torch.float32, (n_pages, page, G), dev), tp)
 
 
 def q8_cache_write(x: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
@@ -590,15 +612,13 @@ def q8_cache_write(x: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor,
         raise ValueError("x must be a CUDA tensor")
     if D > 1 and x.stride(2) != 1:
         raise ValueError("the values of a row of x must be contiguous")
-    code, n_pages, page, Dc, group, max_pages = _cache_args(cache, scales, block_table, B)
+    dev = x.device
+    code, n_pages, page, Dc, group, max_pages, cp, sp, tp = _cache_args(cache, scales, block_table, B, dev)
     if Dc != D:
         raise ValueError(f"x has rows of {D} values, the cache of {Dc}")
-    _want(start, "start", torch.int32, (B,))
-    _want(n_new, "n_new", torch.int32, (B,))
-    _want(err, "err", torch.int32)
-    _on(x.device, cache=cache, scales=scales, start=start, n_new=n_new, block_table=block_table, err=err)
-    st = _call(_lib.sai_q8_cache_write, x.device, _ptr(x), t, x.stride(0), x.stride(1), _ptr(start), _ptr(n_new),
-               _ptr(block_table), B, n, D, group, code, n_pages, page, max_pages, _ptr(cache), _ptr(scales), _ptr(err))
+    st = _call(_lib.sai_q8_cache_write, dev, x.data_ptr(), t, x.stride(0), x.stride(1),
+               _opt(start, "start", torch.int32, (B,), dev), _opt(n_new, "n_new", torch.int32, (B,), dev), tp, B, n, D,
+               group, code, n_pages, page, max_pages, cp, sp, _err(err, dev))
     _check(st, "sai_q8_cache_write")
 
 
@@ -623,20 +643,16 @@ def q8_cache_read(cache: torch.Tensor, scales: torch.Tensor, idx: Optional[torch
         B = block_table.shape[0]
     else:
         B = cache.shape[0]
-    code, n_pages, page, D, group, max_pages = _cache_args(cache, scales, block_table, B)
-    n = max_pages * page if n is None else int(n)
-    _want(idx, "idx", torch.int32, (B, n))
-    _want(start, "start", torch.int32, (B,))
-    _want(lens, "lens", torch.int32, (B,))
-    _want(err, "err", torch.int32)
     dev = cache.device
-    _on(dev, scales=scales, idx=idx, start=start, lens=lens, block_table=block_table, err=err, out=out)
+    code, n_pages, page, D, group, max_pages, cp, sp, tp = _cache_args(cache, scales, block_table, B, dev)
+    n = max_pages * page if n is None else int(n)
+    ip = _opt(idx, "idx", torch.int32, (B, n), dev)
+    fp = _opt(start, "start", torch.int32, (B,), dev)
+    lp = _opt(lens, "lens", torch.int32, (B,), dev)
     if out is None:
         out = torch.empty((B, n, D), dtype=dtype, device=dev)
-    _want(out, "out", dtype, (B, n, D))
-    st = _call(_lib.sai_q8_cache_read, dev, _ptr(cache), _ptr(scales), _ptr(idx), _ptr(start), _ptr(lens),
-               _ptr(block_table), B, n, D, group, code, n_pages, page, max_pages, _ptr(out), _ROW_TYPES[dtype],
-               _ptr(err))
+    st = _call(_lib.sai_q8_cache_read, dev, cp, sp, ip, fp, lp, tp, B, n, D, group, code, n_pages, page, max_pages,
+               _need(out, "out", dtype, (B, n, D), dev), _ROW_TYPES[dtype], _err(err, dev))
     _check(st, "sai_q8_cache_read")
     return out
 
@@ -673,16 +689,15 @@ def q8_quantize(x: torch.Tensor, group: Optional[int] = None, fmt: torch.dtype =
 
 
 def _index_inputs(q8, q_scale, w):
-    """Checked 8-bit queries: (B, S, H, D)."""
+    """Checked 8-bit queries: B, S, H, D and the pointers of the three."""
     if q8.dim() != 4:
         raise ValueError(f"q8 must be [B,S,H,D], got {tuple(q8.shape)}")
     B, S, H, D = q8.shape
-    _want(q8, "q8", torch.int8)
-    if tuple(q_scale.shape) not in ((B, S, H), (B, S, H, 1)):
+    dev = q8.device
+    if q_scale.shape != (B, S, H) and q_scale.shape != (B, S, H, 1):
         raise ValueError(f"q_scale must be [B,S,H] (one scale a row), got {tuple(q_scale.shape)}")
-    _want(q_scale, "q_scale", torch.float32)
-    _want(w, "w", torch.float32, (B, S, H))
-    return B, S, H, D
+    return (B, S, H, D, _need(q8, "q8", torch.int8, (B, S, H, D), dev),
+            _need(q_scale, "q_scale", torch.float32, q_scale.shape, dev), _need(w, "w", torch.float32, (B, S, H), dev))
 
 
 def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cache: torch.Tensor,
@@ -696,10 +711,11 @@ def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cac
     [n_pages,page] (q8_cache_write, one scale a row; without a block_table
     [B,P,D] and [B,P]). P None: every entry of the table. Decoding: S = 1,
     q_start the tokens' positions, k_len the entries each cache holds."""
-    B, S, H, D = _index_inputs(q8, q_scale, w)
+    B, S, H, D, qp, qsp, wp = _index_inputs(q8, q_scale, w)
+    dev = q8.device
     if k_scale.dim() == 2:
         k_scale = k_scale.unsqueeze(2)
-    code, n_pages, page, Dk, group, max_pages = _cache_args(cache, k_scale, block_table, B)
+    code, n_pages, page, Dk, group, max_pages, cp, sp, tp = _cache_args(cache, k_scale, block_table, B, dev)
     if code != 0:
         raise TypeError("cache must be int8")
     if Dk != D or group != D:
@@ -707,19 +723,12 @@ def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cac
     if block_table is None and n_pages != B:
         raise ValueError(f"cache must be [B,P,D] with B = {B} without a block_table, got {tuple(cache.shape)}")
     P = max_pages * page if P is None else int(P)
-    _want(q_start, "q_start", torch.int32, (B,))
-    _want(k_len, "k_len", torch.int32, (B,))
-    _want(doc_start, "doc_start", torch.int32, (B, S))
-    _want(err, "err", torch.int32)
-    dev = q8.device
-    _on(dev, q_scale=q_scale, w=w, cache=cache, k_scale=k_scale, block_table=block_table, q_start=q_start,
-        k_len=k_len, doc_start=doc_start, out=out, err=err)
     if out is None:
         out = torch.empty((B, S, P), dtype=torch.float32, device=dev)
-    _want(out, "out", torch.float32, (B, S, P))
-    st = _call(_lib.sai_indexer_scores, dev, _ptr(q8), _ptr(q_scale), _ptr(w), _ptr(cache), _ptr(k_scale),
-               _ptr(block_table), _ptr(q_start), _ptr(k_len), _ptr(doc_start), B, S, H, D, P, n_pages, page,
-               max_pages, int(cr), _ptr(out), _ptr(err))
+    st = _call(_lib.sai_indexer_scores, dev, qp, qsp, wp, cp, sp, tp, _opt(q_start, "q_start", torch.int32, (B,), dev),
+               _opt(k_len, "k_len", torch.int32, (B,), dev), _opt(doc_start, "doc_start", torch.int32, (B, S), dev), B, S,
+               H, D, P, n_pages, page, max_pages, int(cr), _need(out, "out", torch.float32, (B, S, P), dev),
+               _err(err, dev))
     _check(st, "sai_indexer_scores")
     return out
 
@@ -727,6 +736,8 @@ def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cac
 def scores_backward_workspace_bytes(B: int, S: int, H: int, D: int, P: int, device=None) -> int:
     """Bytes of scratch that sai_indexer_scores_backward needs on `device`."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.index == _current_device():
+        return int(_lib.sai_indexer_scores_backward_workspace_bytes(B, S, H, D, P))
     with torch.cuda.device(dev):
         return int(_lib.sai_indexer_scores_backward_workspace_bytes(B, S, H, D, P))
 
@@ -743,38 +754,30 @@ def indexer_scores_backward(dscores: torch.Tensor, idx: Optional[torch.Tensor], 
     selected blocks idx [B,S,K] (distill_kl's and indexer_topk's outputs; idx
     None: dscores [B,S,P] on every block). q8, q_scale, k8 [B,P,D] and k_scale
     [B,P] are the forward's codes, its activation checkpoints."""
-    B, S, H, D = _index_inputs(q8, q_scale, w)
+    B, S, H, D, qp, qsp, wp = _index_inputs(q8, q_scale, w)
+    dev = q8.device
     if k8.dim() != 3 or k8.shape[0] != B or k8.shape[2] != D:
         raise ValueError(f"k8 must be [B,P,D] with B = {B}, D = {D}, got {tuple(k8.shape)}")
     P = k8.shape[1]
-    _want(k8, "k8", torch.int8)
-    if tuple(k_scale.shape) not in ((B, P), (B, P, 1)):
+    if k_scale.shape != (B, P) and k_scale.shape != (B, P, 1):
         raise ValueError(f"k_scale must be [B,P], got {tuple(k_scale.shape)}")
-    _want(k_scale, "k_scale", torch.float32)
     K = P if idx is None else idx.shape[-1]
-    _want(dscores, "dscores", torch.float32, (B, S, K))
-    _want(idx, "idx", torch.int32, (B, S, K))
-    _want(doc_start, "doc_start", torch.int32, (B, S))
-    _want(err, "err", torch.int32)
-    dev = q8.device
     need = scores_backward_workspace_bytes(B, S, H, D, P, dev)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _want(workspace, "workspace", torch.uint8)
     if dq is None:
         dq = torch.empty((B, S, H, D), dtype=torch.bfloat16, device=dev)
     if dk is None:
         dk = torch.empty((B, P, D), dtype=torch.bfloat16, device=dev)
     if dw is None:
         dw = torch.empty((B, S, H), dtype=torch.float32, device=dev)
-    _want(dq, "dq", torch.bfloat16, (B, S, H, D))
-    _want(dk, "dk", torch.bfloat16, (B, P, D))
-    _want(dw, "dw", torch.float32, (B, S, H))
-    _on(dev, dscores=dscores, idx=idx, q_scale=q_scale, w=w, k8=k8, k_scale=k_scale, doc_start=doc_start,
-        workspace=workspace, dq=dq, dk=dk, dw=dw, err=err)
-    st = _call(_lib.sai_indexer_scores_backward, dev, _ptr(dscores), _ptr(idx), _ptr(q8), _ptr(q_scale), _ptr(w),
-               _ptr(k8), _ptr(k_scale), _ptr(doc_start), B, S, H, D, P, K, int(cr), int(t_begin), _ptr(dq), _ptr(dk),
-               _ptr(dw), _ptr(workspace), workspace.numel(), _ptr(err))
+    st = _call(_lib.sai_indexer_scores_backward, dev, _need(dscores, "dscores", torch.float32, (B, S, K), dev),
+               _opt(idx, "idx", torch.int32, (B, S, K), dev), qp, qsp, wp, _need(k8, "k8", torch.int8, (B, P, D), dev),
+               _need(k_scale, "k_scale", torch.float32, k_scale.shape, dev),
+               _opt(doc_start, "doc_start", torch.int32, (B, S), dev), B, S, H, D, P, K, int(cr), int(t_begin),
+               _need(dq, "dq", torch.bfloat16, (B, S, H, D), dev), _need(dk, "dk", torch.bfloat16, (B, P, D), dev),
+               _need(dw, "dw", torch.float32, (B, S, H), dev),
+               _need(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(), _err(err, dev))
     _check(st, "sai_indexer_scores_backward")
     return dq, dk, dw
 
