@@ -16,14 +16,14 @@
 // of one token are 32 consecutive outputs.
 //
 // Bound: the epilogue. A 128 x 256 tile of D = 128 is 512 cycles of MMA, but its
-// 32,768 products each take an integer instruction (relu and conversion in one),
-// a subtraction and an fma on the four schedulers, 768 issue cycles, between
-// tensor-memory loads whose latency two warps a scheduler hide only in part:
-// about 1,900 cycles a tile measured. Taken from there: the column weights are
-// held in registers over an item's tiles (as broadcasts from shared memory they
-// fill 1,024 cycles a tile with register bytes: 0.56 ms against 0.48 at S = 16384),
-// the next tile is asked for before the last columns are added. At one token
-// a sequence a tile has HP columns and the keys' arrival binds.
+// 32,768 products each take an integer instruction (relu and conversion in one)
+// and half of a packed subtraction and of a packed fma: about 800 cycles with the
+// tensor-memory loads on the four schedulers (measured alone), 1,700 with a
+// tile's hand-overs. Taken from there: the column weights are held in registers
+// over an item's tiles (as broadcasts from shared memory they fill 1,024 cycles a
+// tile with register bytes: 0.56 ms against 0.46 at S = 16384), and a tile's two
+// barriers are tested together. At one token a sequence a tile has HP columns and
+// the keys' arrival binds.
 //
 // One CTA per SM walks work items (sequence, TT tokens, a range of key tiles).
 // Warp roles (384 threads): warp 0 brings key tiles into a ring (TMA; a tile of
@@ -93,16 +93,24 @@ constexpr int kScItemReaders = 2 + kScEpiWarps;
 // Adds the products of four accumulator words and their weights to four partial
 // sums; where a token ends, hands the sums over and clears them.
 template <class End>
-__device__ __forceinline__ void add_heads(const uint32_t *x, const float *w, float (&s)[4], bool ends, End end)
+__device__ __forceinline__ void add_heads(const uint32_t *x, uint64_t w0, uint64_t w1, uint64_t (&s)[2], bool ends,
+                                          End end)
 {
     // max(x + M, M) with M the bits of 2^23 is the fp32 number 2^23 + relu(x), and
     // 2^23 comes off exactly
+    constexpr int M = 0x4B000000;
+    const uint64_t off = pack2(-8388608.f, -8388608.f);
+    float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        s[i] = fmaf(__int_as_float(__viaddmax_s32((int)x[i], 0x4B000000, 0x4B000000)) - 8388608.f, w[i], s[i]);
+        y[i] = __int_as_float(__viaddmax_s32((int)x[i], M, M));
+    s[0] = fma2(add2(pack2(y[0], y[1]), off), w0, s[0]);
+    s[1] = fma2(add2(pack2(y[2], y[3]), off), w1, s[1]);
     if (ends) {
-        end((s[0] + s[1]) + (s[2] + s[3]));
-        s[0] = s[1] = s[2] = s[3] = 0.f;
+        float a, b;
+        unpack2(add2(s[0], s[1]), a, b);
+        end(a + b);
+        s[0] = s[1] = 0u;
     }
 }
 
@@ -442,16 +450,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
             // the group's column weights stay in registers over the item's tiles
             // (a broadcast from shared memory costs as many cycles as the
             // register bytes it fills: 1024 a tile, twice the MMA)
-            float w[GC];
+            uint64_t w[GC / 2];                  // pairs
             int lo[kRegBounds ? T : 1], hi[kRegBounds ? T : 1], end[kRegBounds ? T : 1];
             if (first < n_live) {
 #pragma unroll
                 for (int c = 0; c < GC; c += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(it.ww + col0 + c);
-                    w[c] = v.x;
-                    w[c + 1] = v.y;
-                    w[c + 2] = v.z;
-                    w[c + 3] = v.w;
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(it.ww + col0 + c);
+                    w[c / 2] = v.x;
+                    w[c / 2 + 1] = v.y;
                 }
                 if (kRegBounds) {
 #pragma unroll
@@ -464,13 +470,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
             int j = (it.k_lo + first) * 128 + r;
             float *o = a.out + ((int64_t)it.b * a.S + it.t0 + cg * T) * a.P + j;
-            bool ready = false;                  // the tile's products were seen to be there
             for (int k = first; k < n_live; k += n_par, j += 128 * n_par, o += 128 * n_par) {
                 const uint32_t use = (uint32_t)(n_tiles + k);
                 const int stage = (int)(use % kScRing);
                 const int buf = (int)(use & acc_mask);
-                // (the scales landed before the products were formed: the second wait only orders the reads)
-                if (!__all_sync(0xffffffffu, ready) &&
+                // (the scales landed before the products were formed: the second test only orders the reads)
+                if (!__all_sync(0xffffffffu, mbar_try_wait_both(&sm->acc_full[buf], (use >> acc_log) & 1u,
+                                                                &sm->k_full[stage], (use / kScRing) & 1u)) &&
                     (!warp_mbar_wait_short(&sm->acc_full[buf], (use >> acc_log) & 1u, abort_flag, a.err) ||
                      !warp_mbar_wait_short(&sm->k_full[stage], (use / kScRing) & 1u, abort_flag, a.err))) {
                     if (j < a.P)
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     if (j < (kRegBounds ? end[kRegBounds ? e : 0] : (e < nt ? a.P : 0)))
                         o[(int64_t)e * a.P] = v;
                 };
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                uint64_t s[2] = {0u, 0u};            // four partial sums
 #pragma unroll
                 for (int c = 0; c < GC; c += 16) {
                     if (c >= n_cols)
@@ -504,22 +510,17 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     if (c + 16 < n_cols) {
                         tmem_ld16(taddr + c + 16, x[(c / 16 + 1) & 1]);
                     } else {
-                        // the accumulator and the scales are free before the last columns are
-                        // added, and the next tile is asked for
+                        // the accumulator and the scales are free before the last columns are added
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&sm->acc_empty[buf]);
                             mbar_arrive(&sm->k_empty[stage]);
                         }
-                        const uint32_t u = use + n_par;
-                        ready = k + n_par < n_live &&
-                                mbar_try_wait(&sm->acc_full[u & acc_mask], (u >> acc_log) & 1u) &&
-                                mbar_try_wait(&sm->k_full[u % kScRing], (u / kScRing) & 1u);
                     }
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
-                        add_heads(v + e, w + c + e, s, (c + e + 4) % HP == 0,
+                        add_heads(v + e, w[(c + e) / 2], w[(c + e) / 2 + 1], s, (c + e + 4) % HP == 0,
                                   [&](float sum) { put((c + e) / HP, sum); });
                 }
                 if (!there && a.err)

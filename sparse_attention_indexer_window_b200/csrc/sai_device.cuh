@@ -85,6 +85,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
+// Both phases at once: the two tests are in flight together.
+__device__ __forceinline__ bool mbar_try_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+        : "memory");
+    return ok != 0;
+}
+
 // As mbar_try_wait, but the thread may stay suspended in hardware for up to
 // `ns` nanoseconds waiting for the phase (it resumes as soon as the phase
 // completes), so a waiting warp does not take issue slots from working ones.
