@@ -475,10 +475,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 const int stage = (int)(use % kScRing);
                 const int buf = (int)(use & acc_mask);
                 // (the scales landed before the products were formed: the second test only orders the reads)
-                if (!__all_sync(0xffffffffu, mbar_try_wait_both(&sm->acc_full[buf], (use >> acc_log) & 1u,
-                                                                &sm->k_full[stage], (use / kScRing) & 1u)) &&
-                    (!warp_mbar_wait_short(&sm->acc_full[buf], (use >> acc_log) & 1u, abort_flag, a.err) ||
-                     !warp_mbar_wait_short(&sm->k_full[stage], (use / kScRing) & 1u, abort_flag, a.err))) {
+                if (!warp_mbar_wait_both(&sm->acc_full[buf], (use >> acc_log) & 1u, &sm->k_full[stage],
+                                         (use / kScRing) & 1u, abort_flag, a.err)) {
                     if (j < a.P)
                         for (int e = 0; e < min(nt, T); ++e)
                             o[(int64_t)e * a.P] = __int_as_float(0x7fc00000);

@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             if (go)
                 fetch();
             const int cb = n & 1;
-            if (!warp_mbar_wait_short(&sm->b_full[stage], phase, abort_flag, a.err) ||
-                !warp_mbar_wait_short(&sm->c_empty[cb], ((n >> 1) & 1) ^ 1u, abort_flag, a.err))
+            if (!warp_mbar_wait_both(&sm->b_full[stage], phase, &sm->c_empty[cb], ((n >> 1) & 1) ^ 1u, abort_flag,
+                                     a.err))
                 break;
             const uint8_t *src = sb + stage * tile8;
             uint8_t *dst = sc + cb * tile16;
@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 }
                 const bool closes = wk.last();
                 go = wk.next(a, p);
-                if (!warp_mbar_wait_short(&sm->g_full[n & 1], (n >> 1) & 1, abort_flag, a.err) ||
-                    !warp_mbar_wait_short(&sm->s_full[i][half], n & 1, abort_flag, a.err))
+                if (!warp_mbar_wait_both(&sm->g_full[n & 1], (n >> 1) & 1, &sm->s_full[i][half], n & 1, abort_flag,
+                                         a.err))
                     break;
                 pass_on(n);
                 tc_fence_after();
@@ -846,13 +846,14 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                         dw[1] = fma2(y23, pack2(w.z, w.w), dw[1]);
                         unpack2(y01, y[0], y[1]);
                         unpack2(y23, y[2], y[3]);
-                        // m as a mask of 16 bits a value (y is 0 or at least 1)
-                        const __half2 h01 = __floats2half2_rn(w.x, w.y), h23 = __floats2half2_rn(w.z, w.w);
-                        const __half2 zero = __half2half2(__ushort_as_half(0));
-                        m[e / 2] = *reinterpret_cast<const uint32_t *>(&h01) &
-                                   __hgt2_mask(__floats2half2_rn(y[0], y[1]), zero);
-                        m[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h23) &
-                                       __hgt2_mask(__floats2half2_rn(y[2], y[3]), zero);
+                        // M = m gk, m = min(y, 1) (y is 0 or at least 1)
+                        const __half2 one = __half2half2(__ushort_as_half(0x3C00));
+                        const __half2 m01 = __hmul2(__floats2half2_rn(w.x, w.y),
+                                                    __hmul2_sat(__floats2half2_rn(y[0], y[1]), one));
+                        const __half2 m23 = __hmul2(__floats2half2_rn(w.z, w.w),
+                                                    __hmul2_sat(__floats2half2_rn(y[2], y[3]), one));
+                        m[e / 2] = *reinterpret_cast<const uint32_t *>(&m01);
+                        m[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&m23);
                     }
                     tmem_st8(ts + c / 2, m);            // these columns have been read
                 }

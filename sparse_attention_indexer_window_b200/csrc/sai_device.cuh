@@ -187,6 +187,15 @@ __device__ __forceinline__ bool warp_mbar_wait_short(uint64_t *bar, uint32_t par
     return __all_sync(0xffffffffu, ok);
 }
 
+// Two barriers by a whole warp, tested together first.
+__device__ __forceinline__ bool warp_mbar_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
+                                                    volatile int *abort_flag, int32_t *err)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait_both(bar0, parity0, bar1, parity1)))
+        return true;
+    return warp_mbar_wait_short(bar0, parity0, abort_flag, err) && warp_mbar_wait_short(bar1, parity1, abort_flag, err);
+}
+
 // Bounded wait used only while unwinding after an abort (short limit, no
 // error reporting): lets in-flight copies land before the CTA exits.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
