@@ -39,8 +39,10 @@
 // through its waits), warps 4..11 and 12..19 the epilogues of the two tiles (two
 // warps for each 32 lanes, 64 columns each). The halves are four chains of
 // products, M, second products and the next products in the same place, so that
-// some are with the tensor pipe while others form M. Warps 20..27 turn B's codes
-// into fp16 (dq: four of them, the other four stage gk). Every wait is bounded;
+// some are with the tensor pipe while others form M. dk: warps 20..27 turn B's
+// codes into scaled fp16; dq takes the keys in fp16 as bwd_prep_kernel wrote them
+// (turned into fp16 tile by tile they cost dq a sixth of its instructions), and
+// warps 20..23 stage gk. Every wait is bounded;
 // on timeout the kernel records SAI_ERR_TIMEOUT and unwinds.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,7 +55,7 @@
 namespace sai {
 namespace {
 
-constexpr int kBwThreads = 896;
+constexpr int bw_threads(bool dq) { return dq ? 768 : 896; }
 constexpr int kBwRing = 3;              // code tiles B in flight
 // Floats between two tokens' staged gk: four more than a tile where a warp's lanes
 // span few tokens, so that they use other banks (with 16 tokens a tile the shared
@@ -102,14 +104,42 @@ __device__ __forceinline__ void token_range(const ScoresBwdArgs &a, int b, int t
     }
 }
 
-// One block a token. With idx: the token's G, gathered in shared memory
+// Sixteen codes as fp16 pairs: a byte x as x + 128 under the exponent of 1024 is
+// 1152 + x in fp16, exactly.
+__device__ __forceinline__ void codes_to_f16(const uint4 &v, uint32_t (&o)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const __half2 off = __floats2half2_rn(-1152.f, -1152.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t u = w[e] ^ 0x80808080u;
+        const uint32_t p01 = __byte_perm(u, 0x64646464u, 0x4140), p23 = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 h01 = __hadd2(*reinterpret_cast<const __half2 *>(&p01), off);
+        const __half2 h23 = __hadd2(*reinterpret_cast<const __half2 *>(&p23), off);
+        o[2 * e] = *reinterpret_cast<const uint32_t *>(&h01);
+        o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h23);
+    }
+}
+
+// One block a token, then blocks that write the keys' codes in fp16 (exact) for
+// dq, 16 a thread. With idx: the token's G, gathered in shared memory
 // kPrepCols columns at a time and written out where it has candidates. A
 // block named by one slot (the selection's case) is a plain store, claimed by a
 // bit; if any block is claimed twice, the columns are gathered again by one
 // thread a block in slot order, so that the sum does not depend on timing.
 __global__ void __launch_bounds__(kPrepThreads)
-    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any, bool vec, int cols)
+    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any, uint4 *k16, bool vec, int cols)
 {
+    if ((int64_t)blockIdx.x >= (int64_t)a.B * a.S) {
+        const int64_t i = ((int64_t)blockIdx.x - (int64_t)a.B * a.S) * kPrepThreads + threadIdx.x;
+        if (i >= (int64_t)a.B * a.P * (a.D / 16))
+            return;
+        uint32_t o[8];
+        codes_to_f16(__ldg(reinterpret_cast<const uint4 *>(a.k8) + i), o);
+        k16[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+        k16[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        return;
+    }
     extern __shared__ float4 prep_smem[];            // [cols] G, [cols / 32] claims
     float *g = reinterpret_cast<float *>(prep_smem);
     uint32_t *claimed = reinterpret_cast<uint32_t *>(g + cols);
@@ -336,7 +366,7 @@ __device__ __forceinline__ bool Walk<1>::set(const ScoresBwdArgs &a, const BwPla
 struct BwSmem {
     uint64_t a_full[2], a_empty[2];
     uint64_t b_full[kBwRing], b_empty[kBwRing];
-    uint64_t c_empty[2];                 // fp16 tiles read
+    uint64_t c_full[2], c_empty[2];      // fp16 tiles: loaded (dq); read
     uint64_t s_full[2][2];               // per stationary tile and half: products there
     uint64_t m_full[2][2][2];            // per tile and half, even and odd steps: M and B2 there
     uint64_t acc_full[2], acc_empty[2];  // per tile: an item's accumulator there; read by both halves
@@ -375,9 +405,9 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c)
 }
 
 template <int MODE, int D, int HP>
-__global__ void __launch_bounds__(kBwThreads, 1)
+__global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                  const ScoresBwdArgs a, const BwPlan p)
+                  const __grid_constant__ CUtensorMap mapC, const ScoresBwdArgs a, const BwPlan p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -392,7 +422,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                                                               // then 1 KB of output a warp
     BwSmem *sm = reinterpret_cast<BwSmem *>(reinterpret_cast<uint8_t *>(sg) +
                                             (MODE == 0 ? gk_bytes(HP) + 16 * 1024 : 0));
-    constexpr int kConv = MODE == 0 ? 4 : 8;           // converting warps
+    constexpr int kConv = MODE == 0 ? 0 : 8;           // converting warps
     const int warp = uniform_warp();
     const int lane = threadIdx.x & 31;
 
@@ -400,6 +430,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->a_full[i], 1);
             mbar_init(&sm->a_empty[i], 2);          // each tile's last products
+            mbar_init(&sm->c_full[i], 1);
             mbar_init(&sm->c_empty[i], 4);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&sm->s_full[i][h], 1);
@@ -437,7 +468,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             tma_prefetch_desc(&mapA);
             tma_prefetch_desc(&mapB);
         }
-        int stage = 0, item = -1;
+        int stage = 0, item = -1, n = 0;
         uint32_t phase = 0, a_used = 0, b_used = 0, b_parity = 0;
         bool ok = true;
         for (bool go = wk.begin(a, p); go; go = wk.next(a, p)) {
@@ -479,12 +510,32 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 stage = 0;
                 phase ^= 1u;
             }
+            if (MODE == 0) {
+                // the same keys in fp16
+                const int cb = n & 1;
+                if (!warp_mbar_wait_short(&sm->c_empty[cb], ((n >> 1) & 1) ^ 1u, abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm->c_full[cb], tile16);
+                    for (int blk = 0; blk < D * 2 / kC; ++blk)
+                        tma_load_3d(sc + cb * tile16 + blk * (128 * kC), &mapC, &sm->c_full[cb], blk * (kC / 2),
+                                    wk.s * 128, wk.b);
+                }
+                __syncwarp();
+            }
+            ++n;
         }
         if (!ok && lane == 0) {
             // let the copies in flight land before the CTA goes
             for (int i = 0; i < kBwRing; ++i)
                 if (b_used & (1u << i))
                     mbar_drain(&sm->b_full[i], (b_parity >> i) & 1u);
+            if (MODE == 0)
+                for (int i = 0; i < 2; ++i)
+                    if (n > i)
+                        mbar_drain(&sm->c_full[i], (uint32_t)((n - 1 - i) / 2) & 1u);
             for (int i = 0; i < 2; ++i)
                 if (a_used & (1u << i)) {
                     const int uses = (item - i + 2) / 2;       // loads asked for into buffer i, or one more
@@ -550,7 +601,10 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             ok = !go || arrive_step();
 #pragma unroll
             for (int hf = 0; hf < 2 && ok; ++hf) {
-                ok = warp_mbar_wait_short(&sm->m_full[i][hf][n & 1], (n >> 1) & 1, abort_flag, a.err);
+                ok = MODE == 0 && hf == 0
+                         ? warp_mbar_wait_both(&sm->m_full[i][hf][n & 1], (n >> 1) & 1, &sm->c_full[n & 1], (n >> 1) & 1,
+                                               abort_flag, a.err)
+                         : warp_mbar_wait_short(&sm->m_full[i][hf][n & 1], (n >> 1) & 1, abort_flag, a.err);
                 // an item's first products overwrite the accumulator: the last item's must
                 // have been read (the first half is there before the second has read it)
                 if (ok && hf == 0 && fresh) {
@@ -579,18 +633,16 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             mbar_drain(&sm->drain[i], 0);
         }
         __syncwarp();
-    } else if (warp >= 20 && warp < 20 + kConv) {
+    } else if (MODE == 1 && warp >= 20) {
         // ------------------------------------------------ codes to fp16
-        const int r = (threadIdx.x - 640) & 127;       // row of the tile; dk: two threads a row
-        constexpr int kChunks = D / 16 / (kConv / 4);  // 16-code chunks a thread
-        const int chunk0 = MODE == 0 ? 0 : ((threadIdx.x - 640) >> 7) * kChunks;
-        const float fw = MODE == 1 ? range_scale(__ldg(p.max + kMaxW), 8) : 1.f;
-        // dk: this row's scale; its parts are loaded a step ahead and put together when used
+        const int r = (threadIdx.x - 640) & 127;       // row of the tile; two threads a row
+        constexpr int kChunks = D / 32;                // 16-code chunks a thread
+        const int chunk0 = ((threadIdx.x - 640) >> 7) * kChunks;
+        const float fw = range_scale(__ldg(p.max + kMaxW), 8);
+        // this row's scale; its parts are loaded a step ahead and put together when used
         float rw = 0.f, rs = 0.f;
         uint32_t ra = 0;
         auto fetch = [&]() {
-            if (MODE == 0)
-                return;
             const int tt = r / HP, h = r % HP;
             const int t = wk.s * TT + tt;
             ra = 0;
@@ -609,7 +661,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             fetch();
         while (go) {
             // (a token without a gradient adds nothing, whatever its weights hold)
-            const float scale = MODE == 1 ? (ra ? rw * rs * fw : 0.f) : 1.f;
+            const float scale = ra ? rw * rs * fw : 0.f;
             go = wk.next(a, p);
             if (go)
                 fetch();
@@ -623,26 +675,17 @@ __global__ void __launch_bounds__(kBwThreads, 1)
             const __half hi = __float2half_rn(scale);
             const __half lo = __float2half_rn(scale - __half2float(hi));
             const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
-            const __half2 off = __floats2half2_rn(-1152.f, -1152.f);
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
                 const int c = chunk0 + k;
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + swz<D>(r, c));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[8];
+                codes_to_f16(v, o);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // byte x as x + 128 under the exponent of 1024: 1152 + x in fp16, exact
-                    const uint32_t u = w[e] ^ 0x80808080u;
-                    const uint32_t p01 = __byte_perm(u, 0x64646464u, 0x4140), p23 = __byte_perm(u, 0x64646464u, 0x4342);
-                    __half2 h01 = __hadd2(*reinterpret_cast<const __half2 *>(&p01), off);
-                    __half2 h23 = __hadd2(*reinterpret_cast<const __half2 *>(&p23), off);
-                    if (MODE == 1) {
-                        h01 = __hfma2(h01, hi2, __hmul2(h01, lo2));
-                        h23 = __hfma2(h23, hi2, __hmul2(h23, lo2));
-                    }
-                    o[2 * e] = *reinterpret_cast<const uint32_t *>(&h01);
-                    o[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h23);
+                for (int e = 0; e < 8; ++e) {
+                    const __half2 h = *reinterpret_cast<const __half2 *>(&o[e]);
+                    const __half2 y = __hfma2(h, hi2, __hmul2(h, lo2));
+                    o[e] = *reinterpret_cast<const uint32_t *>(&y);
                 }
                 // 16 values are two 16-byte chunks of the row's fp16 block
                 const uint32_t ch = 2 * c, blk = ch / (kC / 16), cc = ch % (kC / 16);
@@ -663,12 +706,12 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 phase ^= 1u;
             }
         }
-    } else if (MODE == 0 && warp >= 24) {
+    } else if (MODE == 0 && warp >= 20) {
         // ------------------------------------------------ dq: gk staged
         // gk of the step's 128 keys and both tiles' tokens: thread = key, one value
         // a token, read from G a step ahead; lane e holds token e's candidates.
         constexpr int NT = 2 * TT;
-        const int r = threadIdx.x - 768;
+        const int r = threadIdx.x - 640;
         const float f = range_scale(__ldg(p.max + kMaxGk), 15);
         float g[NT], ksv = 0.f;
         int lo = 0, hi = 0;
@@ -826,11 +869,14 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 pass_on(n);
                 tc_fence_after();
                 const float *gk = sg + ((n & 1) * 2 * TT + i * TT + tt) * kBwRow + half * 64;
+                uint32_t x[2][16];
+                tmem_ld16(ts, x[0]);
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(ts + c, v);
+                    const uint32_t(&v)[16] = x[(c / 16) & 1];
                     tmem_ld_wait();
+                    if (c + 16 < 64)
+                        tmem_ld16(ts + c + 16, x[(c / 16 + 1) & 1]);
                     uint32_t m[8];
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
@@ -1052,12 +1098,28 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, 
 
 size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
 
+// fp16 rows [B][P][D], 128 rows a box, in blocks of their swizzle span.
+bool make_map_f16(CUtensorMap *m, const void *ptr, int D, int P, int B)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc)
+        return false;
+    cuuint64_t gdim[3] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)B};
+    cuuint64_t gstride[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * P};
+    cuuint32_t box[3] = {(cuuint32_t)(D < 64 ? D : 64), 128, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(ptr), gdim, gstride, box, estride,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int HP>
-cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
+cudaError_t run_bwd(const ScoresBwdArgs &a, const void *k16, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
                     cudaStream_t st)
 {
-    CUtensorMap rows, keys;    // query rows (HP heads of TT tokens) and keys, 128 rows a box
-    if (!make_map_q8(&rows, a.q8, D, a.H, (uint64_t)a.B * a.S, HP, 128 / HP) ||
+    CUtensorMap rows, keys, keys16;    // query rows (HP heads of TT tokens) and keys, 128 rows a box
+    if (!make_map_f16(&keys16, k16, D, a.P, a.B) ||
+        !make_map_q8(&rows, a.q8, D, a.H, (uint64_t)a.B * a.S, HP, 128 / HP) ||
         !make_map_q8(&keys, a.k8, D, a.P, a.B, 128, 1))
         return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel<0, D, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1067,23 +1129,23 @@ cudaError_t run_bwd(const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, 
                                  (int)bw_smem_bytes<D>(false, HP));
     if (e != cudaSuccess)
         return e;
-    bwd_tc_kernel<0, D, HP><<<grid_q, kBwThreads, bw_smem_bytes<D>(true, HP), st>>>(rows, keys, a, pq);
+    bwd_tc_kernel<0, D, HP><<<grid_q, bw_threads(true), bw_smem_bytes<D>(true, HP), st>>>(rows, keys, keys16, a, pq);
     if (grid_k > 0)
-        bwd_tc_kernel<1, D, HP><<<grid_k, kBwThreads, bw_smem_bytes<D>(false, HP), st>>>(keys, rows, a, pk);
+        bwd_tc_kernel<1, D, HP><<<grid_k, bw_threads(false), bw_smem_bytes<D>(false, HP), st>>>(keys, rows, keys16, a, pk);
     bwd_reduce_kernel<<<(unsigned)(a.B * a.P), 256, 0, st>>>(a, pk, grid_k);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run_bwd_heads(int hp, const ScoresBwdArgs &a, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
+cudaError_t run_bwd_heads(int hp, const ScoresBwdArgs &a, const void *k16, const BwPlan &pq, const BwPlan &pk, int grid_q, int grid_k,
                           cudaStream_t st)
 {
     switch (hp) {
-    case 8: return run_bwd<D, 8>(a, pq, pk, grid_q, grid_k, st);
-    case 16: return run_bwd<D, 16>(a, pq, pk, grid_q, grid_k, st);
-    case 32: return run_bwd<D, 32>(a, pq, pk, grid_q, grid_k, st);
-    case 64: return run_bwd<D, 64>(a, pq, pk, grid_q, grid_k, st);
-    default: return run_bwd<D, 128>(a, pq, pk, grid_q, grid_k, st);
+    case 8: return run_bwd<D, 8>(a, k16, pq, pk, grid_q, grid_k, st);
+    case 16: return run_bwd<D, 16>(a, k16, pq, pk, grid_q, grid_k, st);
+    case 32: return run_bwd<D, 32>(a, k16, pq, pk, grid_q, grid_k, st);
+    case 64: return run_bwd<D, 64>(a, k16, pq, pk, grid_q, grid_k, st);
+    default: return run_bwd<D, 128>(a, k16, pq, pk, grid_q, grid_k, st);
     }
 }
 
@@ -1099,11 +1161,12 @@ int dk_shares(int B, int S, int H, int P)
 
 }  // namespace
 
-// Workspace: the largest magnitudes, a word a token, dk's partial sums, and G.
+// Workspace: the largest magnitudes, a word a token, dk's partial sums, the keys in
+// fp16, and G.
 size_t indexer_scores_bwd_ws_bytes(int B, int S, int H, int D, int P)
 {
     const size_t slots = (size_t)dk_shares(B, S, H, P) + (size_t)B * ((P + 255) / 256);
-    return kMaxWords * 4 + up16((size_t)B * S * 4) + slots * 256 * D * 4 + (size_t)B * S * P * 4;
+    return kMaxWords * 4 + up16((size_t)B * S * 4) + slots * 256 * D * 4 + (size_t)B * P * D * 2 + (size_t)B * S * P * 4;
 }
 
 cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStream_t stream)
@@ -1124,7 +1187,8 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
         ++pk.tt_log;
     pk.n_steps_seq = (a.S + tt - 1) / tt;
     pk.n_pairs = (a.P + 255) / 256;
-    float *G = part + ((size_t)shares + (size_t)a.B * pk.n_pairs) * 256 * a.D;
+    uint4 *k16 = reinterpret_cast<uint4 *>(part + ((size_t)shares + (size_t)a.B * pk.n_pairs) * 256 * a.D);
+    float *G = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(k16) + (size_t)a.B * a.P * a.D * 2);
     pk.G = a.idx ? G : a.dscores;
     pk.max = gmax;
     pk.row = row_any;
@@ -1151,12 +1215,14 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     // rows of idx, dscores, G and k_scale on 16-byte boundaries
     const bool vec = a.idx && a.K % 4 == 0 && a.P % 4 == 0 && al16(a.idx) && al16(a.dscores) && al16(a.k_scale);
     const int cols = a.idx ? (a.P < kPrepCols ? (a.P + 31) / 32 * 32 : kPrepCols) : 32;
-    bwd_prep_kernel<<<a.B * a.S, kPrepThreads, (size_t)cols * 4 + cols / 8, stream>>>(a, G, gmax, row_any, vec, cols);
+    const int64_t key_blocks = ((int64_t)a.B * a.P * (a.D / 16) + kPrepThreads - 1) / kPrepThreads;
+    bwd_prep_kernel<<<(unsigned)((int64_t)a.B * a.S + key_blocks), kPrepThreads, (size_t)cols * 4 + cols / 8, stream>>>(
+        a, G, gmax, row_any, k16, vec, cols);
     if (a.D == 32)
-        return run_bwd_heads<32>(hp, a, pq, pk, grid_q, shares, stream);
+        return run_bwd_heads<32>(hp, a, k16, pq, pk, grid_q, shares, stream);
     if (a.D == 64)
-        return run_bwd_heads<64>(hp, a, pq, pk, grid_q, shares, stream);
-    return run_bwd_heads<128>(hp, a, pq, pk, grid_q, shares, stream);
+        return run_bwd_heads<64>(hp, a, k16, pq, pk, grid_q, shares, stream);
+    return run_bwd_heads<128>(hp, a, k16, pq, pk, grid_q, shares, stream);
 }
 
 }  // namespace sai
