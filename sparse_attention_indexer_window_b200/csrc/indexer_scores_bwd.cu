@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
             constexpr uint32_t kNone = 0xffffffffu;
             uint32_t row = kNone, old_row = kNone;      // B S H fits 31 bits
             float wq = 0.f, qs = 0.f, old_wq = 0.f, old_dw = 0.f;
-            bool any = false, old_any = false, pending = false;
+            bool any = false, pending = false;
             uint64_t dw[2] = {0u, 0u};                  // two fp32 sums each
             auto finish = [&]() -> bool {
                 if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
@@ -812,39 +812,43 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 pending = false;
                 tc_fence_after();
                 if (!half && old_row != kNone)
-                    a.dw[old_row] = old_any ? old_dw + sm->dw[i][r] : 0.f;
+                    a.dw[old_row] = old_dw + sm->dw[i][r];
                 // 16 values of the warp's 32 rows at a time, through shared memory: two
                 // lanes store one row's 32 bytes, not 32 lanes 16 bytes of 32 rows
-                uint32_t dst[2];
+                uint4 *dst[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    dst[e] = __shfl_sync(0xffffffffu, old_row, e * 16 + (lane >> 1));
-#pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(ta + c, v);
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t to = __shfl_sync(0xffffffffu, old_row, e * 16 + (lane >> 1));
+                    dst[e] = to == kNone ? nullptr
+                                         : reinterpret_cast<uint4 *>(a.dq + (int64_t)to * D + half * (D / 2)) + (lane & 1);
+                }
+                uint4 *put0 = out + lane * 2 + ((lane >> 2) & 1), *put1 = out + lane * 2 + (((lane >> 2) & 1) ^ 1);
+                const int l0 = lane >> 1, u = (lane & 1) ^ ((l0 >> 2) & 1);
+                const uint4 *get0 = out + l0 * 2 + u, *get1 = get0 + 32;
+                constexpr int kCh = D / 2 / 16;          // 16-column pieces
+                uint32_t v[2][16];
+                tmem_ld16(ta, v[0]);
+#pragma unroll
+                for (int k = 0; k < kCh; ++k) {
                     tmem_ld_wait();
-                    __syncwarp();
+                    if (k + 1 < kCh)
+                        tmem_ld16(ta + (k + 1) * 16, v[(k + 1) & 1]);
+                    uint32_t o[8];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y0 = __uint_as_float(v[u * 8 + 2 * e]) * old_wq;
-                            const float y1 = __uint_as_float(v[u * 8 + 2 * e + 1]) * old_wq;
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
-                            o[e] = old_any ? *reinterpret_cast<const uint32_t *>(&y) : 0u;
-                        }
-                        out[lane * 2 + (u ^ ((lane >> 2) & 1))] = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int e = 0; e < 8; ++e) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(v[k & 1][2 * e]) * old_wq,
+                                                                       __uint_as_float(v[k & 1][2 * e + 1]) * old_wq);
+                        o[e] = *reinterpret_cast<const uint32_t *>(&y);
                     }
                     __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int l = e * 16 + (lane >> 1), u = lane & 1;
-                        const uint4 o = out[l * 2 + (u ^ ((l >> 2) & 1))];
-                        if (dst[e] != kNone)
-                            *reinterpret_cast<uint4 *>(a.dq + (int64_t)dst[e] * D + half * (D / 2) + c + u * 8) = o;
-                    }
+                    *put0 = make_uint4(o[0], o[1], o[2], o[3]);
+                    *put1 = make_uint4(o[4], o[5], o[6], o[7]);
+                    __syncwarp();
+                    const uint4 r0 = *get0, r1 = *get1;
+                    if (dst[0])
+                        dst[0][k * 2] = r0;
+                    if (dst[1])
+                        dst[1][k * 2] = r1;
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -917,8 +921,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 if (closes) {
                     pending = true;
                     old_row = row;
-                    old_any = any;
-                    old_wq = wq;
+                    old_wq = any ? wq : 0.f;     // (without a gradient the accumulator is 0, and stays 0)
                     float d0, d1;
                     unpack2(add2(dw[0], dw[1]), d0, d1);
                     old_dw = any ? (d0 + d1) * qs : 0.f;
