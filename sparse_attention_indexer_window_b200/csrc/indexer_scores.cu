@@ -157,7 +157,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
     // accumulators in turn: two of 256 columns, or four of 128
     const int acc_log = cols > 128 ? 1 : 2;
     const uint32_t acc_cols = 512u >> acc_log;
-    const int n_mine = (p.n_items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    // One item of every gridDim.x. Whole token tiles come longest first and are taken
+    // there and back: the CTA with the longest of one round takes the shortest of the
+    // next (always from the same end, the first CTA had 35 key tiles at S = 4096 where
+    // the mean is 31: 42.4 us against 40.8). Split ones have no such order (a decoding
+    // batch takes 42.2 us as it is, 43.6 there and back).
+    const int rounds = p.n_items / (int)gridDim.x, back = p.chunk == p.n_kt;
+    auto item_of = [&](int n) {
+        return n * (int)gridDim.x + ((n & back) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    };
+    const int n_mine = rounds + (item_of(rounds) < p.n_items ? 1 : 0);
 
     if (warp < 4) {
     regs_dec<80>();
@@ -334,7 +343,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             const uint32_t iphase = (uint32_t)(n / kScItems) & 1u;
             // chunks outermost, later tokens (more candidates) first: the items of
             // one CTA are spread over tokens, sequences and chunks
-            const int i = (int)blockIdx.x + n * (int)gridDim.x;
+            const int i = item_of(n);
             const int c = i / tiles, tile = i - c * tiles;
             const int b = tile % a.B;
             const int t0 = (p.n_tt - 1 - tile / a.B) * p.tt;
