@@ -22,15 +22,17 @@
 // tile's hand-overs. Taken from there: the column weights are held in registers
 // over an item's tiles (as broadcasts from shared memory they fill 1,024 cycles a
 // tile with register bytes: 0.56 ms against 0.46 at S = 16384), and a tile's two
-// barriers are tested together. At one token a sequence a tile has HP columns and
-// the keys' arrival binds.
+// barriers are tested together. At few tokens a sequence a tile has few columns, and
+// the producers' instructions and the keys' arrival bind.
 //
 // One CTA per SM walks work items (sequence, TT tokens, a range of key tiles).
 // Warp roles (384 threads): warp 0 brings key tiles into a ring (TMA; a tile of
 // a paged cache page by page) with their scales (bulk copies, or cp.async where
-// rows have no 16-byte boundary, completing on the same barrier), warp 1 issues the MMAs, warps 2 and 3 prepare alternate items
-// ahead of the others (bounds, query tile by TMA, the columns' weights) and
-// fill their outputs that have no candidate with -inf, warps 4..7 and 8..11 are
+// rows have no 16-byte boundary, completing on the same barrier), warp 1 issues the
+// MMAs, warps 2 and 3 prepare alternate items ahead of the others (bounds, query
+// tile by TMA, the columns' weights) and fill their outputs that have no candidate
+// with -inf (where the keys are split, warp 2 prepares every item and warp 3 brings
+// every other key tile), warps 4..7 and 8..11 are
 // two epilogue groups taking alternate tiles, each with its own 256-column
 // accumulator. Nothing in the epilogue waits for global memory: at one 0.3 us
 // tile every load there would cost more than the tile. Tiles without a
@@ -49,7 +51,7 @@ constexpr int kScEpiWarps = 8;
 constexpr int kScThreads = 128 + 32 * kScEpiWarps;
 constexpr int kScCols = 256;        // accumulator columns of a tile, at most
 constexpr int kScMaxTok = 32;       // tokens a tile (HP = 8)
-constexpr int kScRing = 7;          // key tiles in flight
+constexpr int kScRing = 6;          // key tiles in flight (even: each belongs to one of two producers)
 constexpr int kScItems = 3;         // items prepared ahead (a query tile each)
 
 struct ScPlan {
@@ -57,6 +59,7 @@ struct ScPlan {
     int n_tt;           // token tiles a sequence
     int n_kt;           // key tiles a sequence
     int chunk;          // key tiles an item
+    int producers;      // warps that bring key tiles: 1, or 2 (of alternate tiles)
     int n_items;
     int groups;         // epilogue groups a tile (128 columns each)
     int box_rows;       // rows of a key load
@@ -86,9 +89,9 @@ struct ScSmem {
     int abort_flag;
 };
 
-// Readers of an item's slot: the key producer, the MMA's completion and the
+// Readers of an item's slot, beside the key producers: the MMA's completion and the
 // epilogue warps.
-constexpr int kScItemReaders = 2 + kScEpiWarps;
+constexpr int kScItemReaders = 1 + kScEpiWarps;
 
 // Adds the products of four accumulator words and their weights to four partial
 // sums; where a token ends, hands the sums over and clears them.
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kScItems; ++i) {
             mbar_init(&sm->i_full[i], 1);
-            mbar_init(&sm->i_empty[i], kScItemReaders);
+            mbar_init(&sm->i_empty[i], kScItemReaders + p.producers);
         }
         for (int s = 0; s < kScRing; ++s) {
             mbar_init(&sm->k_full[s], p.bulk ? 1 : 1 + 32);   // the tile's bytes; each lane's scales
@@ -170,11 +173,12 @@ __global__ void __launch_bounds__(kScThreads, 1)
 
     if (warp < 4) {
     regs_dec<80>();
-    if (warp == 0) {
-        // ------------------------------------------------ key producer
+    if (warp == 0 || (warp == 3 && p.producers == 2)) {
+        // ------------------------------------------------ key producer(s)
         if (lane == 0)
             tma_prefetch_desc(&mapK);
-        int stage = 0, slot = 0;
+        const int mine = warp ? 1 : 0, step = p.producers;
+        int stage = mine, slot = 0, n_tiles = 0;
         uint32_t phase = 0, iphase = 0, k_used = 0, k_parity = 0;
         bool ok = true;
         // tile row i*32 + lane comes with load from[i], as its row off[i] (several loads a tile)
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             const int per = 32 / p.loads, sub = lane % p.loads;
             int ahead = -1, ahead_row = 0, batch = -1, batch_row = 0;
             auto find = [&](int kb) {
-                const int k = kb + lane / p.loads, j0 = k * 128 + sub * p.box_rows;
+                const int k = kb + step * (lane / p.loads), j0 = k * 128 + sub * p.box_rows;
                 ahead = -1;
                 ahead_row = 0;
                 if (k >= k_hi || j0 >= n_keys || lane >= per * p.loads)
@@ -216,13 +220,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     ahead = __ldg(a.map.table + (int64_t)b * a.map.max_pages + pi);
                 }
             };
-            find(k_lo);
+            // (of two producers each takes every other tile of all items' tiles)
+            const int first_k = k_lo + ((n_tiles ^ mine) & (step - 1));
+            n_tiles += k_hi - k_lo;
+            find(first_k);
             int in = per;                             // tile within the batch
-            for (int k = k_lo; k < k_hi; ++k) {
+            for (int k = first_k; k < k_hi; k += step) {
                 if (in == per) {
                     batch = ahead;
                     batch_row = ahead_row;
-                    find(k + per);
+                    find(k + step * per);
                     in = 0;
                 }
                 const int at = in * p.loads + (lane < p.loads ? lane : 0);
@@ -267,8 +274,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 }
                 k_used |= 1u << stage;
                 k_parity = (k_parity & ~(1u << stage)) | (phase << stage);
-                if (++stage == kScRing) {
-                    stage = 0;
+                if ((stage += step) >= kScRing) {
+                    stage = mine;
                     phase ^= 1u;
                 }
             }
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
         const int tiles = a.B * p.n_tt;
         uint32_t q_used = 0, q_parity = 0;
         bool ok = true;
-        for (int n = warp - 2; n < n_mine && ok; n += 2) {
+        for (int n = warp - 2; n < n_mine && ok; n += 3 - p.producers) {
             const int slot = n % kScItems;
             const uint32_t iphase = (uint32_t)(n / kScItems) & 1u;
             // chunks outermost, later tokens (more candidates) first: the items of
@@ -627,15 +634,25 @@ cudaError_t launch_indexer_scores(const ScoresArgs &a, cudaStream_t stream)
     p.n_tt = (a.S + p.tt - 1) / p.tt;
     p.n_kt = (a.P + 127) / 128;
     // Few token tiles (decoding): the keys are split too, into about eight items
-    // an SM. With four token tiles an SM or more their unequal lengths even out
+    // an SM, but an item has four key tiles where that leaves two an SM (at one tile an
+    // item the items' preparation bound: 32 x 2 tokens over 8192 entries took 23 us, 16
+    // with four). With four token tiles an SM or more their unequal lengths even out
     // over the CTAs, and an item's query tile is best read once.
     const long long rows = (long long)a.B * p.n_tt;
-    const long long chunk = rows >= 4LL * sms ? p.n_kt : rows * p.n_kt / (8LL * sms);
+    const long long two = rows * p.n_kt / (2LL * sms), least = two < 4 ? two : 4;
+    long long chunk = rows >= 4LL * sms ? p.n_kt : rows * p.n_kt / (8LL * sms);
+    if (chunk < least)
+        chunk = least;
     p.chunk = (int)(chunk < 1 ? 1 : (chunk > p.n_kt ? p.n_kt : chunk));
     const long long items = rows * ((p.n_kt + p.chunk - 1) / p.chunk);
     if (items > INT32_MAX - 65536)
         return cudaErrorInvalidValue;
     p.n_items = (int)items;
+    // Split items have few columns a tile, so that one producer's 1,150 cycles a tile
+    // bound them (32 x 2 tokens over 16 to 33 thousand entries: 42.5 us, 38.5 with two);
+    // whole ones are better served by two warps that prepare items (a packed batch:
+    // 25.9 us, 30.4 with one).
+    p.producers = p.chunk < p.n_kt && p.chunk >= 2 ? 2 : 1;
     p.box_rows = a.map.page < 128 ? a.map.page : 128;
     p.loads = a.map.max_pages > 1 && a.map.page < 128 ? 128 / a.map.page : 1;
     p.groups = p.tt * hp > 128 ? 2 : 1;
