@@ -112,6 +112,41 @@ def test_paged_cache_and_single_tokens(sai, B, S, H, D, page, pages, P):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("B,S,H,D,page,pages,P,bad", [
+    (4, 1, 64, 128, 64, 320, 20000, False), (5, 2, 8, 32, 8, 2600, 20800, True), (6, 1, 24, 64, 128, 150, 19111, True),
+    (5, 1, 16, 64, 16, 1300, 20790, False), (5, 3, 64, 128, 20001, 1, 20001, False), (9, 1, 128, 32, 32, 640, 20480, True),
+])
+def test_long_caches_of_few_tokens(sai, B, S, H, D, page, pages, P, bad):
+    """Few tokens over many entries, whose keys are split over the SMs: an empty
+    cache between full ones, lengths inside a tile, a page id outside the cache."""
+    q8, qs, w, k8, ks = inputs(P + B, B, S, H, D, P)
+    r = np.random.default_rng(P - B)
+    k_len = np.array([P, 0, P - 77, 129, P // 2 + 3, 1, P, 4000, P - 1][:B], np.int32)
+    q_start = (k_len.astype(np.int64) * 4 + 8).astype(np.int32)
+    n_pages = B * pages + 1
+    table = r.permutation(n_pages)[:B * pages].astype(np.int32).reshape(B, pages)
+    cache = r.integers(-127, 128, (n_pages, page, D)).astype(np.int8)
+    scale = np.full((n_pages, page), np.nan, np.float32)
+    for b in range(B):
+        for i in range((k_len[b] + page - 1) // page):
+            n = min(page, k_len[b] - i * page)
+            cache[table[b, i], :n] = k8[b, i * page:i * page + n]
+            scale[table[b, i], :n] = ks[b, i * page:i * page + n]
+    mask = ref.candidates(B, S, P, 4, q_start, k_len)
+    if bad:
+        i = (P // 2) // page
+        table[0, i] = n_pages
+        mask[0, :, i * page:(i + 1) * page] = False
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = dev(q8, qs, w, cache, scale, table, q_start, k_len)
+    outs = [torch.full((B, S, P), float("nan"), device="cuda") for _ in range(3)]
+    for out in outs:
+        sai.indexer_scores(*a[:5], 4, P=P, block_table=a[5], q_start=a[6], k_len=a[7], out=out, err=err)
+    check(outs[0], q8, qs, w, k8, ks, mask)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert int(err.item()) == (sai.SAI_ERR_INDEX if bad else 0)
+
+
 def test_page_ids_outside_the_cache(sai):
     B, S, H, D, page = 2, 1, 16, 64, 16
     q8, qs, w, k8, ks = inputs(5, B, S, H, D, 64)
