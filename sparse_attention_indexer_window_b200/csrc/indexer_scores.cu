@@ -52,6 +52,7 @@ constexpr int kScThreads = 128 + 32 * kScEpiWarps;
 constexpr int kScCols = 256;        // accumulator columns of a tile, at most
 constexpr int kScMaxTok = 32;       // tokens a tile (HP = 8)
 constexpr int kScRing = 6;          // key tiles in flight (even: each belongs to one of two producers)
+static_assert(kScRing % 2 == 0, "a stage belongs to one producer");
 constexpr int kScItems = 3;         // items prepared ahead (a query tile each)
 
 struct ScPlan {
