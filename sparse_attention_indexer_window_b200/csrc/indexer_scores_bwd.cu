@@ -29,8 +29,10 @@
 //       w qs q8, scaled by row as the codes are turned into fp16.
 //
 // fp16's 11 bits (a rounding of 2^-11 of each term, below the bf16 outputs'
-// 2^-8) hold the operands after one common power of two brings the largest to
-// the top of its range; what falls out at the other end is below 2^-39 of it.
+// 2^-8) hold the operands after a power of two brings the largest to the top of
+// its range; what falls out at the other end is below 2^-39 of it. gk has a power of
+// two for each token (with one for all, a token's dq was lost where its gradients were
+// 2^-35 of another's); G and w qs have one each.
 //
 // Bound: per 128 x 128 tile of D = 128, 256 cycles of kind::i8 and 512 of
 // kind::f16 on the tensor pipe. The two stationary tiles alternate: while one's
@@ -64,7 +66,8 @@ constexpr int gk_row(int hp) { return hp == 8 ? 128 : 132; }
 constexpr int kPrepThreads = 128;
 constexpr int kPrepCols = 4096;         // columns of G gathered at once, at most
 
-// Largest magnitudes, as bits: |G ks|, |G|, |w qs| of tokens with a gradient.
+// Largest magnitudes, as bits: |G ks| of a token; |G|, |w qs| of all tokens with a
+// gradient.
 enum { kMaxGk = 0, kMaxG = 1, kMaxW = 2, kMaxWords = 4 };
 
 struct BwPlan {
@@ -75,7 +78,7 @@ struct BwPlan {
     int share, rest;       // dk: steps of a CTA; the first `rest` CTAs take one more
     const float *G;        // [B,S,P]
     const uint32_t *max;   // kMaxWords
-    const uint32_t *row;   // [B,S] not 0 where the token has a gradient
+    const float *row;      // [B,S] scale of the token's gk; 0 where it has no gradient
     float *part;           // dk: [grid + B n_pairs][256][D]
 };
 
@@ -89,6 +92,9 @@ __device__ __forceinline__ float range_scale(uint32_t bits, int top)
     frexpf(__uint_as_float(bits), &e);            // magnitude in [2^(e-1), 2^e)
     return ldexpf(1.f, max(-120, min(120, top - e)));
 }
+
+// 1 / f of a power of two that range_scale returned.
+__device__ __forceinline__ float inverse_pow2(float f) { return __uint_as_float((254u << 23) - __float_as_uint(f)); }
 
 // Candidates [lo, hi) of the token at local index t (its position fits 31 bits:
 // checked on the host).
@@ -128,7 +134,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4 &v, uint32_t (&o)[8])
 // bit; if any block is claimed twice, the columns are gathered again by one
 // thread a block in slot order, so that the sum does not depend on timing.
 __global__ void __launch_bounds__(kPrepThreads)
-    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, uint32_t *row_any, uint4 *k16, bool vec, int cols)
+    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, float *row_scale, uint4 *k16, bool vec, int cols)
 {
     if ((int64_t)blockIdx.x >= (int64_t)a.B * a.S) {
         const int64_t i = ((int64_t)blockIdx.x - (int64_t)a.B * a.S) * kPrepThreads + threadIdx.x;
@@ -271,10 +277,10 @@ __global__ void __launch_bounds__(kPrepThreads)
             v = max(v, buf[threadIdx.x][i]);
             any |= buf[3][i];
         }
-        if (threadIdx.x == 3)
-            row_any[row] = any;
+        if (threadIdx.x == kMaxGk)
+            row_scale[row] = any ? range_scale(v, 15) : 0.f;
         // (a stale word only means one more atomic)
-        else if (any && v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
+        else if (threadIdx.x < 3 && any && v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
             atomicMax(gmax + threadIdx.x, v);
     }
 }
@@ -650,11 +656,11 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
         const float fw = range_scale(__ldg(p.max + kMaxW), 8);
         // this row's scale; its parts are loaded a step ahead and put together when used
         float rw = 0.f, rs = 0.f;
-        uint32_t ra = 0;
+        float ra = 0.f;
         auto fetch = [&]() {
             const int tt = r / HP, h = r % HP;
             const int t = wk.s * TT + tt;
-            ra = 0;
+            ra = 0.f;
             rw = rs = 0.f;
             if (t < a.S && h < a.H) {
                 const int64_t row = (int64_t)wk.b * a.S + t;
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
             fetch();
         while (go) {
             // (a token without a gradient adds nothing, whatever its weights hold)
-            const float scale = ra ? rw * rs * fw : 0.f;
+            const float scale = ra != 0.f ? rw * rs * fw : 0.f;
             go = wk.next(a, p);
             if (go)
                 fetch();
@@ -718,18 +724,19 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
     } else if (MODE == 0 && warp >= 20) {
         // ------------------------------------------------ dq: gk staged
         // gk of the step's 128 keys and both tiles' tokens: thread = key, one value
-        // a token, read from G a step ahead; lane e holds token e's candidates.
+        // a token, read from G a step ahead; lane e holds token e's candidates and scale.
         constexpr int NT = 2 * TT;
         const int r = threadIdx.x - 640;
-        const float f = range_scale(__ldg(p.max + kMaxGk), 15);
-        float g[NT], ksv = 0.f;
+        float g[NT], ksv = 0.f, f = 0.f;
         int lo = 0, hi = 0;
         auto fetch = [&]() {
             if (wk.first) {
                 const int t = wk.a0 + lane;
                 lo = hi = 0;
-                if (lane < NT && t < a.S)
+                if (lane < NT && t < a.S) {
                     token_range(a, wk.b, t, lo, hi);
+                    f = __ldg(p.row + (int64_t)wk.b * a.S + t);
+                }
             }
             const int j = wk.s * 128 + r;
             ksv = j < a.P ? __ldg(a.k_scale + (int64_t)wk.b * a.P + j) : 0.f;
@@ -749,8 +756,10 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 break;
             float *dst = sg + (n & 1) * NT * kBwRow + r;
 #pragma unroll
-            for (int e = 0; e < NT; ++e)
-                dst[e * kBwRow] = g[e] != 0.f ? g[e] * ksv * f : 0.f;
+            for (int e = 0; e < NT; ++e) {
+                const float fe = __shfl_sync(0xffffffffu, f, e);
+                dst[e * kBwRow] = g[e] != 0.f ? g[e] * ksv * fe : 0.f;
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm->g_full[n & 1]);
@@ -782,7 +791,6 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
         };
         int n = 0, items = 0;
         if constexpr (MODE == 0) {
-            const float inv = 1.f / range_scale(__ldg(p.max + kMaxGk), 15);
             const int tt = r / HP, h = r % HP;
             uint4 *out = reinterpret_cast<uint4 *>(sg + 4 * TT * kBwRow) + (warp - 4) * 64;
             // Items without a candidate never reach the walk: their gradients are zero.
@@ -870,7 +878,9 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 if (wk.first) {
                     const int t = wk.a0 + i * TT + tt;
                     row = t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
-                    any = row != kNone && __ldg(p.row + (int64_t)wk.b * a.S + t) != 0u;
+                    const float f = row != kNone ? __ldg(p.row + (int64_t)wk.b * a.S + t) : 0.f;
+                    any = f != 0.f;
+                    const float inv = any ? inverse_pow2(f) : 0.f;
                     wq = row != kNone ? __ldg(a.w + row) * inv : 0.f;
                     qs = row != kNone ? __ldg(a.q_scale + row) * inv : 0.f;
                 }
@@ -1191,7 +1201,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     int shares = dk_shares(a.B, a.S, a.H, a.P);
     uint8_t *w = static_cast<uint8_t *>(ws);
     uint32_t *gmax = reinterpret_cast<uint32_t *>(w);
-    uint32_t *row_any = reinterpret_cast<uint32_t *>(w + kMaxWords * 4);
+    float *row_scale = reinterpret_cast<float *>(w + kMaxWords * 4);
     float *part = reinterpret_cast<float *>(w + kMaxWords * 4 + up16((size_t)a.B * a.S * 4));
     BwPlan pk;
     pk.tt_log = 0;
@@ -1203,7 +1213,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     float *G = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(k16) + (size_t)a.B * a.P * a.D * 2);
     pk.G = a.idx ? G : a.dscores;
     pk.max = gmax;
-    pk.row = row_any;
+    pk.row = row_scale;
     pk.part = part;
     long long per_seq = 0;
     for (int kp = 0; kp < pk.n_pairs; ++kp) {
@@ -1229,7 +1239,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     const int cols = a.idx ? (a.P < kPrepCols ? (a.P + 31) / 32 * 32 : kPrepCols) : 32;
     const int64_t key_blocks = ((int64_t)a.B * a.P * (a.D / 16) + kPrepThreads - 1) / kPrepThreads;
     bwd_prep_kernel<<<(unsigned)((int64_t)a.B * a.S + key_blocks), kPrepThreads, (size_t)cols * 4 + cols / 8, stream>>>(
-        a, G, gmax, row_any, k16, vec, cols);
+        a, G, gmax, row_scale, k16, vec, cols);
     if (a.D == 32)
         return run_bwd_heads<32>(hp, a, k16, pq, pk, grid_q, shares, stream);
     if (a.D == 64)
