@@ -635,6 +635,10 @@ sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const floa
  * dw is fp32 throughout. In dq a term's m G k_scale is held in fp16, scaled by
  * the token's largest |G k_scale|, and the terms are added in fp32: a term is
  * off by at most 2^-11 of itself and 2^-39 of the token's largest (times 127).
+ * In dk both m G and w q_scale q8 are, the one scaled by the key's largest
+ * |G| max_h|w q_scale|, the other by the token's largest |w q_scale|: a term is
+ * off by at most 2^-10 of itself and 2^-32 of the largest that the key has and
+ * that the token's heads have (times 127).
  *
  *   dscores  [B,S,K] fp32 (sai_distill_kl's); idx [B,S,K] int32, or NULL
  *            (K = P); an entry outside {-1} U [0,P) is ignored and sets

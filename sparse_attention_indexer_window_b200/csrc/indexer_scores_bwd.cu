@@ -11,7 +11,7 @@
 // the gradients with respect to the values that the codes stand for.
 //
 // Launches: bwd_prep_kernel writes G densely (slots of one block added in slot
-// order) with the largest magnitudes; bwd_tc_kernel<dq> and <dk>; and
+// order) with each token's and each key's largest magnitudes; bwd_tc_kernel<dq> and <dk>; and
 // bwd_reduce_kernel adds dk's partial sums in a fixed order. Nothing depends on
 // timing: the same inputs give the same bits.
 //
@@ -31,8 +31,9 @@
 // fp16's 11 bits (a rounding of 2^-11 of each term, below the bf16 outputs'
 // 2^-8) hold the operands after a power of two brings the largest to the top of
 // its range; what falls out at the other end is below 2^-39 of it. gk has a power of
-// two for each token (with one for all, a token's dq was lost where its gradients were
-// 2^-35 of another's); G and w qs have one each.
+// two for each token, w qs one for each token, and G, times that one's inverse, one for
+// each key: with one for the batch, a token's dq and a key's dk were lost where their
+// gradients were 2^-35 of others'.
 //
 // Bound: per 128 x 128 tile of D = 128, 256 cycles of kind::i8 and 512 of
 // kind::f16 on the tensor pipe. The two stationary tiles alternate: while one's
@@ -65,10 +66,10 @@ constexpr int kBwRing = 3;              // code tiles B in flight
 constexpr int gk_row(int hp) { return hp == 8 ? 128 : 132; }
 constexpr int kPrepThreads = 128;
 constexpr int kPrepCols = 4096;         // columns of G gathered at once, at most
-
-// Largest magnitudes, as bits: |G ks| of a token; |G|, |w qs| of all tokens with a
-// gradient.
-enum { kMaxGk = 0, kMaxG = 1, kMaxW = 2, kMaxWords = 4 };
+// Each key's largest magnitude is kept by so many groups of tokens apart (every
+// eighth token): the first blocks all raise every word, and at one word a key their
+// atomics took as long as the rest of the kernel (S = 4096: 26 us, 14 with eight).
+constexpr int kKeyGroups = 8;
 
 struct BwPlan {
     int tt_log;            // tokens a 128-row tile, as a power of two
@@ -77,8 +78,10 @@ struct BwPlan {
     int per_seq;           // dk: steps of one sequence
     int share, rest;       // dk: steps of a CTA; the first `rest` CTAs take one more
     const float *G;        // [B,S,P]
-    const uint32_t *max;   // kMaxWords
-    const float *row;      // [B,S] scale of the token's gk; 0 where it has no gradient
+    const uint32_t *key;   // [kKeyGroups,B,P] the key's largest |G| times the token's power of two for
+                           // w qs, as bits
+    const float2 *row;     // [B,S] scale of the token's gk, the power of two above its |w qs|; 0, 0 where
+                           // it has no gradient
     float *part;           // dk: [grid + B n_pairs][256][D]
 };
 
@@ -93,8 +96,22 @@ __device__ __forceinline__ float range_scale(uint32_t bits, int top)
     return ldexpf(1.f, max(-120, min(120, top - e)));
 }
 
-// 1 / f of a power of two that range_scale returned.
+// 1 / f of a power of two of at least 2^-126, at most 2^126.
 __device__ __forceinline__ float inverse_pow2(float f) { return __uint_as_float((254u << 23) - __float_as_uint(f)); }
+
+// dk's factors are scaled by token and by key: with u the power of two above the
+// token's largest |w qs| (kept where 256 / u is a normal number), B2 is w qs q8 256 / u,
+// below 2^15 (2^16 in the last binade, still fp16), and M is G u f, f the power of two that
+// brings the key's largest |G| u below 2^15.
+__device__ __forceinline__ float weight_pow2(uint32_t bits)
+{
+    return __uint_as_float(max(8u, min(254u, (bits >> 23) + 1u)) << 23);
+}
+__device__ __forceinline__ float weight_scale(float u) { return __uint_as_float((262u << 23) - __float_as_uint(u)); }
+__device__ __forceinline__ float key_scale(uint32_t bits)
+{
+    return __uint_as_float(min(253u, 268u - (bits >> 23)) << 23);
+}
 
 // Candidates [lo, hi) of the token at local index t (its position fits 31 bits:
 // checked on the host).
@@ -134,7 +151,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4 &v, uint32_t (&o)[8])
 // bit; if any block is claimed twice, the columns are gathered again by one
 // thread a block in slot order, so that the sum does not depend on timing.
 __global__ void __launch_bounds__(kPrepThreads)
-    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *gmax, float *row_scale, uint4 *k16, bool vec, int cols)
+    bwd_prep_kernel(const ScoresBwdArgs a, float *G, uint32_t *key_max, float2 *row_scale, uint4 *k16, bool vec, int cols)
 {
     if ((int64_t)blockIdx.x >= (int64_t)a.B * a.S) {
         const int64_t i = ((int64_t)blockIdx.x - (int64_t)a.B * a.S) * kPrepThreads + threadIdx.x;
@@ -149,7 +166,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     extern __shared__ float4 prep_smem[];            // [cols] G, [cols / 32] claims
     float *g = reinterpret_cast<float *>(prep_smem);
     uint32_t *claimed = reinterpret_cast<uint32_t *>(g + cols);
-    __shared__ uint32_t buf[4][kPrepThreads / 32];
+    __shared__ uint32_t buf[3][kPrepThreads / 32];    // largest |w qs|, |G ks|; any gradient at all
     const int64_t row = blockIdx.x;
     const int b = (int)(row / a.S);
     const int t = (int)(row - (int64_t)b * a.S);
@@ -160,33 +177,61 @@ __global__ void __launch_bounds__(kPrepThreads)
         const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
         return u < 0x7f800000u ? u : 0u;
     };
-    uint32_t top[4] = {0u, 0u, 0u, 0u};              // kMaxGk, kMaxG, kMaxW; any gradient at all
     const float *ks = a.k_scale + (int64_t)b * a.P;
     const float *ds = a.dscores + row * a.K;
-    auto seen = [&](float v, float scale) {
-        if (v != 0.f) {
-            top[3] = 1u;
-            top[kMaxG] = max(top[kMaxG], finite(v));
-            top[kMaxGk] = max(top[kMaxGk], finite(v * scale));
-        }
-    };
-    // (H <= 128: one value a thread, loaded ahead)
+    const int32_t *idx = a.idx ? a.idx + row * a.K : nullptr;
+    // the first slots, on their way while the weights are looked at
+    int4 id0 = make_int4(-1, -1, -1, -1);
+    float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool first = vec && (int)threadIdx.x < a.K / 4;
+    if (first) {
+        id0 = __ldg(reinterpret_cast<const int4 *>(idx) + threadIdx.x);
+        v0 = __ldg(reinterpret_cast<const float4 *>(ds) + threadIdx.x);
+    }
+    // (H <= 128: one value a thread)
     const bool has_h = (int)threadIdx.x < a.H;
     const float wv = has_h ? __ldg(a.w + row * a.H + threadIdx.x) : 0.f;
     const float qv = has_h ? __ldg(a.q_scale + row * a.H + threadIdx.x) : 0.f;
+    const uint32_t top_w = __reduce_max_sync(0xffffffffu, finite(wv * qv));
+    if ((threadIdx.x & 31) == 0)
+        buf[0][threadIdx.x >> 5] = top_w;
+    __syncthreads();
+    uint32_t w_bits = 0;
+#pragma unroll
+    for (int i = 0; i < kPrepThreads / 32; ++i)
+        w_bits = max(w_bits, buf[0][i]);
+    const float u = weight_pow2(w_bits);
+    uint32_t top_gk = 0u, any = 0u;
+    uint32_t *km = key_max + ((int64_t)(t & (kKeyGroups - 1)) * a.B + b) * a.P;
+    auto seen = [&](float v, float scale) {
+        if (v != 0.f) {
+            any = 1u;
+            top_gk = max(top_gk, finite(v * scale));
+        }
+    };
+    // Largest of the keys [j0, j1), of which key j has the gradient of(j): only a
+    // largest value's binade is used, so a word is written where the binade rises (a
+    // stale word only means one more atomic). Four words a thread on their way at once.
+    auto keys_seen = [&](int j0, int j1, auto of) {
+        for (int j = j0 + threadIdx.x; j < j1; j += 4 * kPrepThreads) {
+            uint32_t had[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                had[e] = j + e * kPrepThreads < j1 ? __ldcg(km + j + e * kPrepThreads) : 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e * kPrepThreads < j1) {
+                    const uint32_t most = finite(of(j + e * kPrepThreads) * u);
+                    if ((most >> 23) > (had[e] >> 23))
+                        atomicMax(km + j + e * kPrepThreads, most);
+                }
+        }
+    };
     if (!a.idx) {
         for (int j = lo + threadIdx.x; j < hi; j += kPrepThreads)
             seen(__ldg(ds + j), __ldg(ks + j));
+        keys_seen(lo, hi, [&](int j) { return __ldg(ds + j); });
     } else {
-        const int32_t *idx = a.idx + row * a.K;
-        // the first slots, on their way while the columns are cleared
-        int4 id0 = make_int4(-1, -1, -1, -1);
-        float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool first = vec && (int)threadIdx.x < a.K / 4;
-        if (first) {
-            id0 = __ldg(reinterpret_cast<const int4 *>(idx) + threadIdx.x);
-            v0 = __ldg(reinterpret_cast<const float4 *>(ds) + threadIdx.x);
-        }
         for (int c0 = lo & ~31; c0 < hi || c0 == (lo & ~31); c0 += cols) {
             const int n = max(0, min(cols, hi - c0));
             for (int j = threadIdx.x; j < n; j += kPrepThreads)
@@ -259,29 +304,25 @@ __global__ void __launch_bounds__(kPrepThreads)
                     seen(v, __ldg(ks + c0 + j));
                 }
             }
+            // (a warp's atomics fall on 32 neighbouring words, however G is written)
+            keys_seen(c0, c0 + n, [&](int j) { return g[j - c0]; });
             __syncthreads();
         }
     }
-    top[kMaxW] = finite(wv * qv);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        top[e] = __reduce_max_sync(0xffffffffu, top[e]);
-        if ((threadIdx.x & 31) == 0)
-            buf[e][threadIdx.x >> 5] = top[e];
+    top_gk = __reduce_max_sync(0xffffffffu, top_gk);
+    any = __reduce_max_sync(0xffffffffu, any);
+    if ((threadIdx.x & 31) == 0) {
+        buf[1][threadIdx.x >> 5] = top_gk;
+        buf[2][threadIdx.x >> 5] = any;
     }
     __syncthreads();
-    if (threadIdx.x < 4) {
-        uint32_t v = 0, any = 0;
+    if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 0; i < kPrepThreads / 32; ++i) {
-            v = max(v, buf[threadIdx.x][i]);
-            any |= buf[3][i];
+        for (int i = 1; i < kPrepThreads / 32; ++i) {
+            top_gk = max(top_gk, buf[1][i]);
+            any |= buf[2][i];
         }
-        if (threadIdx.x == kMaxGk)
-            row_scale[row] = any ? range_scale(v, 15) : 0.f;
-        // (a stale word only means one more atomic)
-        else if (threadIdx.x < 3 && any && v > *reinterpret_cast<volatile uint32_t *>(gmax + threadIdx.x))
-            atomicMax(gmax + threadIdx.x, v);
+        row_scale[row] = any ? make_float2(range_scale(top_gk, 15), u) : make_float2(0.f, 0.f);
     }
 }
 
@@ -653,18 +694,15 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
         const int r = (threadIdx.x - 640) & 127;       // row of the tile; two threads a row
         constexpr int kChunks = D / 32;                // 16-code chunks a thread
         const int chunk0 = ((threadIdx.x - 640) >> 7) * kChunks;
-        const float fw = range_scale(__ldg(p.max + kMaxW), 8);
         // this row's scale; its parts are loaded a step ahead and put together when used
-        float rw = 0.f, rs = 0.f;
-        float ra = 0.f;
+        float rw = 0.f, rs = 0.f, ru = 0.f;
         auto fetch = [&]() {
             const int tt = r / HP, h = r % HP;
             const int t = wk.s * TT + tt;
-            ra = 0.f;
-            rw = rs = 0.f;
+            rw = rs = ru = 0.f;
             if (t < a.S && h < a.H) {
                 const int64_t row = (int64_t)wk.b * a.S + t;
-                ra = __ldg(p.row + row);
+                ru = __ldg(&p.row[row].y);
                 rw = __ldg(a.w + row * a.H + h);
                 rs = __ldg(a.q_scale + row * a.H + h);
             }
@@ -676,7 +714,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
             fetch();
         while (go) {
             // (a token without a gradient adds nothing, whatever its weights hold)
-            const float scale = ra != 0.f ? rw * rs * fw : 0.f;
+            const float scale = ru != 0.f ? rw * rs * weight_scale(ru) : 0.f;
             go = wk.next(a, p);
             if (go)
                 fetch();
@@ -735,7 +773,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 lo = hi = 0;
                 if (lane < NT && t < a.S) {
                     token_range(a, wk.b, t, lo, hi);
-                    f = __ldg(p.row + (int64_t)wk.b * a.S + t);
+                    f = __ldg(&p.row[(int64_t)wk.b * a.S + t].x);
                 }
             }
             const int j = wk.s * 128 + r;
@@ -878,7 +916,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 if (wk.first) {
                     const int t = wk.a0 + i * TT + tt;
                     row = t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
-                    const float f = row != kNone ? __ldg(p.row + (int64_t)wk.b * a.S + t) : 0.f;
+                    const float f = row != kNone ? __ldg(&p.row[(int64_t)wk.b * a.S + t].x) : 0.f;
                     any = f != 0.f;
                     const float inv = any ? inverse_pow2(f) : 0.f;
                     wq = row != kNone ? __ldg(a.w + row) * inv : 0.f;
@@ -950,19 +988,24 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
             if (pending && ok)
                 finish();
         } else {
-            const float fg = range_scale(__ldg(p.max + kMaxG), 15);
-            const float inv = 1.f / fg, inv_w = 1.f / range_scale(__ldg(p.max + kMaxW), 8);
             // this key's gradients of the tokens of the warp's columns, read a step
-            // ahead; lane e holds token e's candidates, [0, hi) kept up by counting
+            // ahead; lane e holds token e's power of two for its weights and its candidates,
+            // [0, hi) kept up by counting
             constexpr int NT = HP > 64 ? 1 : TT / 2;    // tokens of 64 columns
             const int e0 = HP > 64 ? 0 : half * NT;
-            float raw[NT];
+            float raw[NT], u_tok = 0.f, f = 0.f;        // f: the key's scale
             int lo = 0, hi = 0, rem = 0;
             const int up = TT / a.cr, up_rem = TT - up * a.cr;
             auto fetch = [&]() {
                 const int j = wk.a0 + i * 128 + r;
                 const int t = wk.s * TT + lane;
                 if (wk.first) {
+                    uint32_t most = 0u;
+#pragma unroll
+                    for (int e = 0; e < kKeyGroups; ++e)
+                        if (j < a.P)
+                            most = max(most, __ldg(p.key + ((int64_t)e * a.B + wk.b) * a.P + j));
+                    f = key_scale(most);
                     const uint32_t ends = (uint32_t)a.t_begin + (uint32_t)t + 1u;
                     hi = (int)(ends / (uint32_t)a.cr);
                     rem = (int)(ends - (uint32_t)hi * (uint32_t)a.cr);
@@ -976,6 +1019,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 }
                 const float *src = p.G + ((int64_t)wk.b * a.S + wk.s * TT + e0) * a.P + j;
                 const int end = t < a.S ? min(a.P, hi) : 0;
+                u_tok = lane < TT && t < a.S ? __ldg(&p.row[(int64_t)wk.b * a.S + t].y) : 0.f;
                 if (a.doc_start) {
                     int l, u;
                     lo = 0;
@@ -997,7 +1041,8 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 uint32_t g[NT];
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
-                    g[e] = __half_as_ushort(__float2half_rn(raw[e] * fg));
+                    g[e] = __half_as_ushort(__float2half_rn(raw[e] * __shfl_sync(0xffffffffu, u_tok, e0 + e) * f));
+                const float inv = inverse_pow2(f);
                 const int pair = wk.pair;
                 const bool closes = wk.last();
                 go = wk.next(a, p);
@@ -1047,9 +1092,9 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
 #pragma unroll
                         for (int e = 0; e < 16; e += 4)
                             *reinterpret_cast<float4 *>(o + c + e) =
-                                make_float4(__uint_as_float(v[e]) * inv * inv_w, __uint_as_float(v[e + 1]) * inv * inv_w,
-                                            __uint_as_float(v[e + 2]) * inv * inv_w,
-                                            __uint_as_float(v[e + 3]) * inv * inv_w);
+                                make_float4(__uint_as_float(v[e]) * 0x1p-8f * inv, __uint_as_float(v[e + 1]) * 0x1p-8f * inv,
+                                            __uint_as_float(v[e + 2]) * 0x1p-8f * inv,
+                                            __uint_as_float(v[e + 3]) * 0x1p-8f * inv);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1183,12 +1228,12 @@ int dk_shares(int B, int S, int H, int P)
 
 }  // namespace
 
-// Workspace: the largest magnitudes, a word a token, dk's partial sums, the keys in
-// fp16, and G.
+// Workspace: each key's largest magnitude, two words a token, dk's partial sums, the
+// keys in fp16, and G.
 size_t indexer_scores_bwd_ws_bytes(int B, int S, int H, int D, int P)
 {
     const size_t slots = (size_t)dk_shares(B, S, H, P) + (size_t)B * ((P + 255) / 256);
-    return kMaxWords * 4 + up16((size_t)B * S * 4) + slots * 256 * D * 4 + (size_t)B * P * D * 2 + (size_t)B * S * P * 4;
+    return up16((size_t)kKeyGroups * B * P * 4) + up16((size_t)B * S * 8) + slots * 256 * D * 4 + (size_t)B * P * D * 2 + (size_t)B * S * P * 4;
 }
 
 cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStream_t stream)
@@ -1200,9 +1245,10 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     const int tt = 128 / hp;
     int shares = dk_shares(a.B, a.S, a.H, a.P);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    uint32_t *gmax = reinterpret_cast<uint32_t *>(w);
-    float *row_scale = reinterpret_cast<float *>(w + kMaxWords * 4);
-    float *part = reinterpret_cast<float *>(w + kMaxWords * 4 + up16((size_t)a.B * a.S * 4));
+    uint32_t *key_max = reinterpret_cast<uint32_t *>(w);
+    const size_t key_bytes = up16((size_t)kKeyGroups * a.B * a.P * 4);
+    float2 *row_scale = reinterpret_cast<float2 *>(w + key_bytes);
+    float *part = reinterpret_cast<float *>(w + key_bytes + up16((size_t)a.B * a.S * 8));
     BwPlan pk;
     pk.tt_log = 0;
     while ((1 << pk.tt_log) < tt)
@@ -1212,7 +1258,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     uint4 *k16 = reinterpret_cast<uint4 *>(part + ((size_t)shares + (size_t)a.B * pk.n_pairs) * 256 * a.D);
     float *G = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(k16) + (size_t)a.B * a.P * a.D * 2);
     pk.G = a.idx ? G : a.dscores;
-    pk.max = gmax;
+    pk.key = key_max;
     pk.row = row_scale;
     pk.part = part;
     long long per_seq = 0;
@@ -1231,7 +1277,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     pq.n_pairs = (a.S + 2 * tt - 1) / (2 * tt);
     const long long items = (long long)a.B * pq.n_pairs;
     const int grid_q = (int)(items < sms ? items : sms);
-    cudaError_t e = cudaMemsetAsync(gmax, 0, kMaxWords * 4, stream);
+    cudaError_t e = cudaMemsetAsync(key_max, 0, key_bytes, stream);
     if (e != cudaSuccess)
         return e;
     // rows of idx, dscores, G and k_scale on 16-byte boundaries
@@ -1239,7 +1285,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     const int cols = a.idx ? (a.P < kPrepCols ? (a.P + 31) / 32 * 32 : kPrepCols) : 32;
     const int64_t key_blocks = ((int64_t)a.B * a.P * (a.D / 16) + kPrepThreads - 1) / kPrepThreads;
     bwd_prep_kernel<<<(unsigned)((int64_t)a.B * a.S + key_blocks), kPrepThreads, (size_t)cols * 4 + cols / 8, stream>>>(
-        a, G, gmax, row_scale, k16, vec, cols);
+        a, G, key_max, row_scale, k16, vec, cols);
     if (a.D == 32)
         return run_bwd_heads<32>(hp, a, k16, pq, pk, grid_q, shares, stream);
     if (a.D == 64)

@@ -83,6 +83,48 @@ def test_tokens_of_small_gradients_keep_their_dq(sai, H, D, dense):
     check_rows(run(sai, ds, idx, q8, qs, w, k8, ks, cr), G, q8, qs, w, k8, ks, ("dq", "dw"))
 
 
+@pytest.mark.parametrize("H,D", SHAPES)
+@pytest.mark.parametrize("dense", [False, True])
+def test_keys_of_small_gradients_keep_their_dk(sai, H, D, dense):
+    """Two documents in a row and two rows: the gradients (or the head weights) of
+    one are 2^-35 or 2^-45 of the other's."""
+    B, S, cr = 2, 160, 4
+    P = S // cr
+    q8, qs, w, k8, ks = inputs(H + D + 1, B, S, H, D, P)
+    doc = np.zeros((B, S), np.int32)
+    doc[:, 80:] = 80
+    mask = ref.candidates(B, S, P, cr, doc_start=doc)
+    if dense:
+        idx, ds = None, np.where(mask, np.random.default_rng(D).standard_normal(mask.shape), 0).astype(np.float32)
+    else:
+        idx, ds = selection(H, mask, 9)
+        ds = np.where(idx >= 0, ds * 1e6, 0).astype(np.float32)
+    ds[0, :80] *= 2.0 ** -35
+    w[1, 80:] *= 2.0 ** -45
+    ds[1] *= 2.0 ** -10
+    G = ref.dense(ds, idx, mask)
+    check_rows(run(sai, ds, idx, q8, qs, w, k8, ks, cr, doc), G, q8, qs, w, k8, ks)
+
+
+def test_a_sequence_alone_and_in_a_batch(sai):
+    """dq and dw of a sequence are the same bits whatever it is batched with."""
+    B, S, H, D, cr = 3, 200, 24, 64, 2
+    P = S // cr
+    q8, qs, w, k8, ks = inputs(30, B, S, H, D, P)
+    mask = ref.candidates(B, S, P, cr)
+    idx, ds = selection(30, mask, 20)
+    ds[1] *= np.float32(2.0 ** 40)
+    ks[2, 5], qs[2, 7] = 2.0 ** 18, 2.0 ** 25
+    whole = run(sai, ds, idx, q8, qs, w, k8, ks, cr)
+    G = ref.dense(ds, idx, mask)
+    for b in range(B):
+        one = [x[b:b + 1] for x in (ds, idx, q8, qs, w, k8, ks)]
+        alone = run(sai, *one, cr)
+        assert torch.equal(alone[0], whole[0][b:b + 1]) and torch.equal(alone[2], whole[2][b:b + 1])
+        check_rows(alone, G[b:b + 1], *one[2:])
+        check_rows([x[b:b + 1] for x in whole], G[b:b + 1], *one[2:])
+
+
 @pytest.mark.parametrize("S,H,D,cr,K", [(1500, 64, 128, 4, 60), (700, 128, 128, 2, 0), (5000, 8, 128, 20, 40)])
 def test_lists_of_items_at_the_full_width(sai, S, H, D, cr, K):
     """D = 128, where tensor memory is full: more items than the GPU has SMs, of one
