@@ -603,7 +603,7 @@ sai_status sai_q8_cache_read(const void *cache, const float *scales, const int32
  *            inside the kernel gave up
  *
  * S = 1 with a block table is the decoding form. Sizes: 1 <= H <= 128, D one
- * of 32, 64, 128, P <= max_pages*page; with more than one page a sequence,
+ * of 32, 64, 128, B*S*H and B*P at most 2^31 - 16385, P <= max_pages*page; with more than one page a sequence,
  * page a multiple of 128 or one of 8, 16, 32, 64. Errors: SAI_ERR_NULL,
  * SAI_ERR_SHAPE, SAI_ERR_ALIGN, SAI_ERR_UNSUPPORTED, SAI_ERR_CUDA.
  */

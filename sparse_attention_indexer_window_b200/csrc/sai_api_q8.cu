@@ -48,7 +48,9 @@ sai_status check_indexer(int B, int S, int H, int D, int P, int cr)
 {
     if (B < 1 || S < 1 || H < 1 || D < 1 || P < 1 || cr < 1)
         return SAI_ERR_SHAPE;
-    if ((int64_t)B * S * H > INT32_MAX || (int64_t)B * P > INT32_MAX || (int64_t)P * cr > INT32_MAX)
+    // (the kernels count rows and keys in 32 bits, up to 64 tiles of 128 past the last)
+    constexpr int64_t most = INT32_MAX - 16384;
+    if ((int64_t)B * S * H > most || (int64_t)B * P > most || (int64_t)P * cr > INT32_MAX)
         return SAI_ERR_SHAPE;
     if (H > 128 || (D != 32 && D != 64 && D != 128))
         return SAI_ERR_UNSUPPORTED;
@@ -149,7 +151,8 @@ sai_status sai_indexer_scores_backward(const float *dscores, const int32_t *idx,
     if (e != SAI_OK)
         return e;
     if (K < 1 || K > P || (!idx && K != P) || t_begin < 0 || (int64_t)t_begin + S > INT32_MAX ||
-        (int64_t)B * ((P + 255LL) / 256) * ((S + 127LL) / 128 * sai::padded_heads(H) + 1) > INT32_MAX)
+        (int64_t)B * ((P + 255LL) / 256) * ((S + 127LL) / 128 * sai::padded_heads(H) + 1) > INT32_MAX ||
+        (int64_t)B * S + ((int64_t)B * P * (D / 16) + 127) / 128 > INT32_MAX)       // blocks of the first kernel
         return SAI_ERR_SHAPE;
     if (!al4(dscores) || (idx && !al4(idx)) || !al16(q8) || !al4(q_scale) || !al4(w) || !al16(k8) ||
         !al4(k_scale) || !al16(dq) || !al16(dk) || !al4(dw) || (doc_start && !al4(doc_start)) ||

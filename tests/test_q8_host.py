@@ -130,3 +130,19 @@ def test_reference_e4m3_grid():
     assert np.array_equal(v, ref.e4m3_values())
     z = np.linspace(-440, 440, 4001)
     assert np.array_equal(ref.e4m3_round(z), torch.from_numpy(z).float().to(torch.float8_e4m3fn).double().numpy())
+
+
+@pytest.mark.parametrize("n", [0, 1, 127, 128, 255, 16383])
+def test_lengths_next_to_the_last_number_of_31_bits(sai, n):
+    """A key, row or block number may not run past 31 bits, in the last tile or in the plan."""
+    big, lib = (1 << 31) - 1 - n, sai.lib()
+    sizes = ((1, 1, 1, 32, big), (1, big, 1, 32, 4), (2, 1, 1, 32, big // 2), (2, big // 2, 1, 32, 4))
+    for B, S, H, D, P in sizes:
+        assert lib.sai_indexer_scores(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, B, S, H, D, P, 1, P, 1, 1,
+                                      FAKE, None, None) == 2, (B, S, H, D, P)
+        assert lib.sai_indexer_scores_backward_workspace_bytes(B, S, H, D, P) == 0, (B, S, H, D, P)
+        assert lib.sai_indexer_scores_backward(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, B, S, H, D, P, 1, 1, 0,
+                                               FAKE, FAKE, FAKE, FAKE, 1 << 60, None, None) == 2, (B, S, H, D, P)
+    # tokens and key blocks together
+    assert lib.sai_indexer_scores_backward(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, 1 << 10, (1 << 21) - 64, 1,
+                                           128, 1 << 20, 1, 1, 0, FAKE, FAKE, FAKE, FAKE, 1 << 60, None, None) == 2
