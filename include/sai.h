@@ -600,7 +600,7 @@ sai_status sai_q8_cache_read(const void *cache, const float *scales, const int32
  *   scores   [B,S,P] fp32, written
  *   d_err    optional: SAI_ERR_INDEX if a candidate's page id lies outside
  *            [0, n_pages) (its scores are -inf), SAI_ERR_TIMEOUT if a wait
- *            inside the kernel gave up
+ *            inside the kernel gave up (scores not formed by then are NaN)
  *
  * S = 1 with a block table is the decoding form. Sizes: 1 <= H <= 128, D one
  * of 32, 64, 128, B*S*H and B*P at most 2^31 - 16385, P <= max_pages*page; with more than one page a sequence,

@@ -37,7 +37,7 @@
 // accumulator. Nothing in the epilogue waits for global memory: at one 0.3 us
 // tile every load there would cost more than the tile. Tiles without a
 // candidate are never multiplied. Every wait is bounded; on timeout the kernel
-// records SAI_ERR_TIMEOUT, writes NaN and unwinds.
+// records SAI_ERR_TIMEOUT and unwinds, and what its CTA had not written is NaN.
 #include <math.h>
 
 #include "indexer_q8.h"
@@ -171,6 +171,15 @@ __global__ void __launch_bounds__(kScThreads, 1)
         return n * (int)gridDim.x + ((n & back) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
     };
     const int n_mine = rounds + (item_of(rounds) < p.n_items ? 1 : 0);
+    // An item's chunk of key tiles, sequence and first token: chunks outermost, later
+    // tokens (more candidates) first, so that the items of one CTA are spread over
+    // tokens, sequences and chunks.
+    auto place_of = [&](int n, int &c, int &b, int &t0) {
+        const int i = item_of(n), tiles = a.B * p.n_tt;
+        c = i / tiles;
+        b = (i - c * tiles) % a.B;
+        t0 = (p.n_tt - 1 - (i - c * tiles) / a.B) * p.tt;
+    };
 
     if (warp < 4) {
     regs_dec<80>();
@@ -343,18 +352,13 @@ __global__ void __launch_bounds__(kScThreads, 1)
         // ------------------------------------------------ items ahead
         if (lane == 0)
             tma_prefetch_desc(&mapQ);
-        const int tiles = a.B * p.n_tt;
         uint32_t q_used = 0, q_parity = 0;
         bool ok = true;
         for (int n = warp - 2; n < n_mine && ok; n += 3 - p.producers) {
             const int slot = n % kScItems;
             const uint32_t iphase = (uint32_t)(n / kScItems) & 1u;
-            // chunks outermost, later tokens (more candidates) first: the items of
-            // one CTA are spread over tokens, sequences and chunks
-            const int i = item_of(n);
-            const int c = i / tiles, tile = i - c * tiles;
-            const int b = tile % a.B;
-            const int t0 = (p.n_tt - 1 - tile / a.B) * p.tt;
+            int c, b, t0;
+            place_of(n, c, b, t0);
             const int ntok = min(p.tt, a.S - t0);
             const int c_lo = c * p.chunk, c_hi = min(p.n_kt, c_lo + p.chunk);
             const int64_t pos = (int64_t)(a.q_start ? __ldg(a.q_start + b) : 0) + t0 + lane;
@@ -454,12 +458,14 @@ __global__ void __launch_bounds__(kScThreads, 1)
         constexpr int T = GC / HP;              // tokens of a group
         constexpr bool kRegBounds = T <= 4;     // their bounds are kept in registers
         const uint32_t acc_mask = (1u << acc_log) - 1;
-        int n_tiles = 0, slot = 0;
+        int n_tiles = 0, slot = 0, n = 0;
         uint32_t iphase = 0;
         bool ok = true;
-        for (int n = 0; n < n_mine && ok; ++n) {
-            if (!warp_mbar_wait_short(&sm->i_full[slot], iphase, abort_flag, a.err))
+        for (; n < n_mine; ++n) {
+            if (!warp_mbar_wait_short(&sm->i_full[slot], iphase, abort_flag, a.err)) {
+                ok = false;
                 break;
+            }
             const ScItem &it = sm->item[slot];
             const int n_live = it.k_hi - it.k_lo;
             const int nt = it.ntok - cg * T;     // tokens from the group's first on
@@ -494,9 +500,6 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 // (the scales landed before the products were formed: the second test only orders the reads)
                 if (!warp_mbar_wait_both(&sm->acc_full[buf], (use >> acc_log) & 1u, &sm->k_full[stage],
                                          (use / kScRing) & 1u, abort_flag, a.err)) {
-                    if (j < a.P)
-                        for (int e = 0; e < min(nt, T); ++e)
-                            o[(int64_t)e * a.P] = __int_as_float(0x7fc00000);
                     ok = false;
                     break;
                 }
@@ -543,6 +546,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         if (j >= it.jlo[cg * T + e] && j < it.jhi[cg * T + e])
                             atomicExch(a.err, kErrIndex);
             }
+            if (!ok)
+                break;
             n_tiles += n_live;
             __syncwarp();
             if (lane == 0)
@@ -551,6 +556,16 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 slot = 0;
                 iphase ^= 1u;
             }
+        }
+        // A wait gave up: NaN for the item it was for and those behind it. (Another warp
+        // may still write a finished tile's scores, or -inf where no candidate is, to them.)
+        for (; !ok && n < n_mine; ++n) {
+            int c, b, t0;
+            place_of(n, c, b, t0);
+            const int ntok = min(p.tt, a.S - t0), j1 = min(a.P, min(p.n_kt, (c + 1) * p.chunk) * 128);
+            for (int tt = 0; tt < ntok; ++tt)
+                for (int j = c * p.chunk * 128 + lane; j < j1; j += 32)
+                    a.out[((int64_t)b * a.S + t0 + tt) * a.P + j] = __int_as_float(0x7fc00000);
         }
     }
 
