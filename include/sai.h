@@ -650,6 +650,8 @@ sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const floa
  *   workspace device scratch of sai_indexer_scores_backward_workspace_bytes()
  *            bytes, 16-byte aligned; its content need not be kept
  *
+ * Where a wait inside a kernel gave up (SAI_ERR_TIMEOUT in *d_err), the rows of
+ * dq and dw that were not formed are NaN, and all of dk.
  * dk of tokens split over calls (t_begin) is the sum of the calls' dk. Errors:
  * as for sai_indexer_scores, and SAI_ERR_WORKSPACE.
  */

@@ -45,8 +45,9 @@
 // some are with the tensor pipe while others form M. dk: warps 20..27 turn B's
 // codes into scaled fp16; dq takes the keys in fp16 as bwd_prep_kernel wrote them
 // (turned into fp16 tile by tile they cost dq a sixth of its instructions), and
-// warps 20..23 stage gk. Every wait is bounded;
-// on timeout the kernel records SAI_ERR_TIMEOUT and unwinds.
+// warps 20..23 stage gk. Every wait is bounded; on timeout the kernel records
+// SAI_ERR_TIMEOUT and unwinds: the rows of dq and dw that were not formed are NaN, and
+// all of dk.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -83,6 +84,7 @@ struct BwPlan {
     const float2 *row;     // [B,S] scale of the token's gk, the power of two above its |w qs|; 0, 0 where
                            // it has no gradient
     float *part;           // dk: [grid + B n_pairs][256][D]
+    uint32_t *gave_up;     // dk: not 0 where a wait gave up
 };
 
 // The power of two that brings a largest magnitude (bits) below 2^top, at
@@ -911,11 +913,15 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                     mbar_arrive(&sm->acc_empty[i]);
                 return true;
             };
+            auto row_of = [&]() {
+                const int t = wk.a0 + i * TT + tt;
+                return t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
+            };
             bool go = wk.begin(a, p), ok = true;
-            while (go && ok) {
+            while (go) {
                 if (wk.first) {
                     const int t = wk.a0 + i * TT + tt;
-                    row = t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
+                    row = row_of();
                     const float f = row != kNone ? __ldg(&p.row[(int64_t)wk.b * a.S + t].x) : 0.f;
                     any = f != 0.f;
                     const float inv = any ? inverse_pow2(f) : 0.f;
@@ -925,8 +931,10 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 const bool closes = wk.last();
                 go = wk.next(a, p);
                 if (!warp_mbar_wait_both(&sm->g_full[n & 1], (n >> 1) & 1, &sm->s_full[i][half], n & 1, abort_flag,
-                                         a.err))
+                                         a.err)) {
+                    ok = false;
                     break;
+                }
                 pass_on(n);
                 tc_fence_after();
                 const float *gk = sg + ((n & 1) * 2 * TT + i * TT + tt) * kBwRow + half * 64;
@@ -967,8 +975,10 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sm->g_empty[n & 1]);
-                if (pending)
-                    ok = finish();
+                if (pending && !finish()) {
+                    ok = false;
+                    break;
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -986,7 +996,28 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 }
             }
             if (pending && ok)
-                finish();
+                ok = finish();
+            // A wait gave up: NaN for the rows of the finished item, the current one and those
+            // behind it.
+            auto spoil = [&](uint32_t to) {
+                if (to == kNone)
+                    return;
+                if (!half)
+                    a.dw[to] = __int_as_float(0x7fc00000);
+                for (int c = 0; c < D / 2; ++c)
+                    a.dq[(int64_t)to * D + half * (D / 2) + c] = 0x7fc0;
+            };
+            if (!ok) {
+                if (pending)
+                    spoil(old_row);
+                spoil(row);
+                while (go) {
+                    if (wk.first)
+                        spoil(row_of());
+                    wk.s = wk.s_end - 1;
+                    go = wk.next(a, p);
+                }
+            }
         } else {
             // this key's gradients of the tokens of the warp's columns, read a step
             // ahead; lane e holds token e's power of two for its weights and its candidates,
@@ -1034,7 +1065,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                     raw[e] = j >= l && j < u ? __ldg(src) : 0.f;
                 }
             };
-            bool go = wk.begin(a, p);
+            bool go = wk.begin(a, p), ok = true;
             if (go)
                 fetch();
             while (go) {
@@ -1048,7 +1079,8 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 go = wk.next(a, p);
                 if (go)
                     fetch();
-                if (!warp_mbar_wait_short(&sm->s_full[i][half], n & 1, abort_flag, a.err))
+                ok = warp_mbar_wait_short(&sm->s_full[i][half], n & 1, abort_flag, a.err);
+                if (!ok)
                     break;
                 pass_on(n);
                 tc_fence_after();
@@ -1078,7 +1110,8 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                     mbar_arrive(&sm->m_full[i][half][n & 1]);
                 ++n;
                 if (closes) {
-                    if (!warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err))
+                    ok = warp_mbar_wait_short(&sm->acc_full[i], items & 1, abort_flag, a.err);
+                    if (!ok)
                         break;
                     ++items;
                     tc_fence_after();
@@ -1102,6 +1135,8 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                         mbar_arrive(&sm->acc_empty[i]);
                 }
             }
+            if (!ok && lane == 0)
+                *p.gave_up = 1u;                // partial sums are missing: no key's dk is right
         }
     }
 
@@ -1113,10 +1148,11 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
     }
 }
 
-// dk: the partial sums of a pair's segments, added in a fixed order. One block a
+// dk: the partial sums of a pair's segments, added in a fixed order (NaN where
+// one is missing). One block a
 // key; the segments are cut into 1024 / D runs of neighbours, whose sums are
 // added in order, so that the loads of a long list are in flight together.
-__global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p, int shares)
+__global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p)
 {
     __shared__ float4 run[256];
     const int b = (int)(blockIdx.x / (unsigned)a.P), j = (int)(blockIdx.x - (unsigned)b * (unsigned)a.P);
@@ -1158,6 +1194,8 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, 
         s.z += v.z;
         s.w += v.w;
     }
+    if (__ldg(p.gave_up) != 0u)
+        s.x = s.y = s.z = s.w = __int_as_float(0x7fc00000);
     const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
     *reinterpret_cast<uint2 *>(a.dk + (int64_t)blockIdx.x * a.D + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
@@ -1199,7 +1237,7 @@ cudaError_t run_bwd(const ScoresBwdArgs &a, const void *k16, const BwPlan &pq, c
     bwd_tc_kernel<0, D, HP><<<grid_q, bw_threads(true), bw_smem_bytes<D>(true, HP), st>>>(rows, keys, keys16, a, pq);
     if (grid_k > 0)
         bwd_tc_kernel<1, D, HP><<<grid_k, bw_threads(false), bw_smem_bytes<D>(false, HP), st>>>(keys, rows, keys16, a, pk);
-    bwd_reduce_kernel<<<(unsigned)(a.B * a.P), 256, 0, st>>>(a, pk, grid_k);
+    bwd_reduce_kernel<<<(unsigned)(a.B * a.P), 256, 0, st>>>(a, pk);
     return cudaGetLastError();
 }
 
@@ -1228,12 +1266,13 @@ int dk_shares(int B, int S, int H, int P)
 
 }  // namespace
 
-// Workspace: each key's largest magnitude, two words a token, dk's partial sums, the
-// keys in fp16, and G.
+// Workspace: four words (the first: a wait gave up), each key's largest magnitude, two
+// words a token, dk's partial sums, the keys in fp16, and G.
+constexpr size_t kStatusBytes = 16;
 size_t indexer_scores_bwd_ws_bytes(int B, int S, int H, int D, int P)
 {
     const size_t slots = (size_t)dk_shares(B, S, H, P) + (size_t)B * ((P + 255) / 256);
-    return up16((size_t)kKeyGroups * B * P * 4) + up16((size_t)B * S * 8) + slots * 256 * D * 4 + (size_t)B * P * D * 2 + (size_t)B * S * P * 4;
+    return kStatusBytes + up16((size_t)kKeyGroups * B * P * 4) + up16((size_t)B * S * 8) + slots * 256 * D * 4 + (size_t)B * P * D * 2 + (size_t)B * S * P * 4;
 }
 
 cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStream_t stream)
@@ -1245,8 +1284,9 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     const int tt = 128 / hp;
     int shares = dk_shares(a.B, a.S, a.H, a.P);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    uint32_t *key_max = reinterpret_cast<uint32_t *>(w);
-    const size_t key_bytes = up16((size_t)kKeyGroups * a.B * a.P * 4);
+    uint32_t *gave_up = reinterpret_cast<uint32_t *>(w);
+    uint32_t *key_max = reinterpret_cast<uint32_t *>(w + kStatusBytes);
+    const size_t key_bytes = kStatusBytes + up16((size_t)kKeyGroups * a.B * a.P * 4);
     float2 *row_scale = reinterpret_cast<float2 *>(w + key_bytes);
     float *part = reinterpret_cast<float *>(w + key_bytes + up16((size_t)a.B * a.S * 8));
     BwPlan pk;
@@ -1259,6 +1299,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     float *G = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(k16) + (size_t)a.B * a.P * a.D * 2);
     pk.G = a.idx ? G : a.dscores;
     pk.key = key_max;
+    pk.gave_up = gave_up;
     pk.row = row_scale;
     pk.part = part;
     long long per_seq = 0;
@@ -1277,7 +1318,7 @@ cudaError_t launch_indexer_scores_bwd(const ScoresBwdArgs &a, void *ws, cudaStre
     pq.n_pairs = (a.S + 2 * tt - 1) / (2 * tt);
     const long long items = (long long)a.B * pq.n_pairs;
     const int grid_q = (int)(items < sms ? items : sms);
-    cudaError_t e = cudaMemsetAsync(key_max, 0, key_bytes, stream);
+    cudaError_t e = cudaMemsetAsync(w, 0, key_bytes, stream);
     if (e != cudaSuccess)
         return e;
     // rows of idx, dscores, G and k_scale on 16-byte boundaries
