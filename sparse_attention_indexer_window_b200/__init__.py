@@ -139,9 +139,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 # The current stream of a device as its handle (a Stream object costs as much
-# as a small launch).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# as a small launch). Where torch lacks these two, as builds without CUDA do, its
+# public calls serve.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(dev: torch.device):

@@ -146,3 +146,20 @@ def test_lengths_next_to_the_last_number_of_31_bits(sai, n):
     # tokens and key blocks together
     assert lib.sai_indexer_scores_backward(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, 1 << 10, (1 << 21) - 64, 1,
                                            128, 1 << 20, 1, 1, 0, FAKE, FAKE, FAKE, FAKE, 1 << 60, None, None) == 2
+
+
+def test_import_without_cuda_in_torch():
+    """A torch built without CUDA has no binding of streams and devices: the
+    package imports there, and refuses on the host as before."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import sparse_attention_indexer_window_b200 as m\n"
+            "assert m.lib().sai_indexer_scores(*[None] * 9, *[1] * 9, *[None] * 3) == 1\n"
+            "assert m.version() > 0\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
