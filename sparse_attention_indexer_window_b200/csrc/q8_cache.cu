@@ -30,6 +30,7 @@
 
 #include "indexer_q8.h"
 #include "sai_device.cuh"
+#include "sai_host.h"
 
 namespace sai {
 namespace {
@@ -374,7 +375,7 @@ RowWalk plan_rows(int64_t n_rows, int vecs, bool &deep, unsigned &blocks)
     while (w.lane_log < 5 && (1 << w.lane_log) < vecs)
         ++w.lane_log;
     const int rp = 32 >> w.lane_log;
-    deep = rp <= 8 && n_rows / (4 * rp) >= 148 * 32;
+    deep = rp <= 8 && n_rows / (4 * rp) >= 32LL * sm_count();
     w.per_warp = deep ? 4 * rp : rp;
     const int64_t per_block = (int64_t)w.per_warp * (kQ8Threads / 32);
     blocks = (unsigned)((n_rows + per_block - 1) / per_block);
