@@ -394,7 +394,7 @@ __device__ __forceinline__ bool Walk<0>::set(const ScoresBwdArgs &a, const BwPla
         first = true;
         if (s_end > 0)
             return true;
-        // no candidate: the epilogue's roles write the zeros (see zero_item)
+        // no candidate: the epilogue writes the zeros before its walk
     }
     return false;
 }
@@ -607,6 +607,11 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
         // waits and one commit; everything else that must be known done (code tiles
         // read, fp16 tiles read) follows from the products of the next step and
         // is passed on by the warps that wait for those. The halves are added in order.
+        // A half's second products (kind::f16) read M from tensor memory, and the next
+        // kind::i8 products are issued behind them, without a wait between, into the columns
+        // that M lies in. This takes it that one thread's tcgen05.mma run in the order of
+        // their issue. The PTX manual promises that for one accumulator and shape, and here
+        // both differ; repeated runs of long lists of items have always given the same bits.
         const int i = warp - 1;
         constexpr uint32_t id_s = idesc_i8_s32(128, 64);
         constexpr uint32_t id_acc = idesc_f16_f32_bmn(128, D);
