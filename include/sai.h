@@ -567,7 +567,9 @@ sai_status sai_q8_cache_write(const void *x, int x_type, int64_t stride_b, int64
  * outside [0, n_pages) or an idx below -1 gives a row of zeros and
  * SAI_ERR_INDEX in *d_err.
  *
- *   idx   [B,n] int32 or NULL (e.g. the selection of sai_indexer_topk);
+ *   idx   [B,n] int32 or NULL: a list of entries a sequence (a token's
+ *         selected blocks: one row a sequence of sai_indexer_topk's idx, or
+ *         the caller's own selection from the scores of single tokens);
  *         start [B] int32 or NULL, only without idx; lens [B] int32 or NULL
  *   out   [B,n,D] of out_type, 16-byte aligned
  *
@@ -586,8 +588,10 @@ sai_status sai_q8_cache_read(const void *cache, const float *scales, const int32
  *
  * for the candidates j of token t, and -inf elsewhere. With pos = q_start[b] +
  * t and d0 = clamp(doc_start[b,t], 0, pos), block j is a candidate iff
- * (j+1)*cr - 1 <= pos, j*cr >= d0 and j < k_len[b] (the rule of
- * sai_indexer_topk, which takes these scores). The products of the codes are
+ * (j+1)*cr - 1 <= pos, j*cr >= d0 and j < k_len[b]. This is the rule of
+ * sai_indexer_topk, which selects from the scores of whole sequences (P*cr = S,
+ * q_start and k_len NULL); it does not take those of single tokens or of part of
+ * a sequence, whose positions it has no argument for. The products of the codes are
  * added exactly, the heads in fp32. Scales must not be negative (those of
  * sai_q8_cache_write are not).
  *

@@ -14,7 +14,7 @@ The indexer in 8 bits, before and after the loss:
     q8_quantize(x)                                             -> (codes, scales)
     q8_cache_write(x, cache, scales, start=, n_new=, block_table=)   rows quantised into a paged cache
     q8_cache_read(cache, scales, idx=, lens=, block_table=)    -> [B,n,D] bf16/fp16/fp32
-    indexer_scores(q8, q_scale, w, cache, k_scale, cr, ...)    -> [B,S,P] fp32, indexer_topk's input
+    indexer_scores(q8, q_scale, w, cache, k_scale, cr, ...)    -> [B,S,P] fp32; of whole sequences indexer_topk's input
     indexer_scores_backward(dscores, idx, q8, q_scale, w, k8, k_scale, cr) -> (dq, dk, dw)
     indexer_distill_step(...)                                  -> (loss, dq, dk, dw), the whole path
 
@@ -708,7 +708,8 @@ def indexer_scores(q8: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, cac
                    k_len: Optional[torch.Tensor] = None, doc_start: Optional[torch.Tensor] = None,
                    out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Scores [B,S,P] of every candidate block through sai_indexer_scores, -inf
-    elsewhere: indexer_topk's input. q8 [B,S,H,D] int8 with q_scale [B,S,H]
+    elsewhere: indexer_topk's input where they are of whole sequences (P*cr = S;
+    it takes no positions of single tokens). q8 [B,S,H,D] int8 with q_scale [B,S,H]
     (q8_quantize), w [B,S,H] fp32; cache [n_pages,page,D] int8 with k_scale
     [n_pages,page] (q8_cache_write, one scale a row; without a block_table
     [B,P,D] and [B,P]). P None: every entry of the table. Decoding: S = 1,
