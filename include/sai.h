@@ -559,7 +559,8 @@ sai_status sai_q8_cache_write(const void *x, int x_type, int64_t stride_b, int64
 /*
  * sai_q8_cache_read -- entries of the cache as 16- or 32-bit rows.
  *
- *   out[b,i,:] = code * scale of entry pos, rounded once to out_type
+ *   out[b,i,:] = code * scale of entry pos, the product in fp32, then rounded to
+ *                out_type (half a step of it and 2^-24 at most from the exact one)
  *   pos = idx[b,i], or (idx NULL) start[b] + i
  *
  * A row of zeros is written where idx is -1 and where pos >= lens[b] (entries
@@ -656,7 +657,9 @@ sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const floa
  *
  * Where a wait inside a kernel gave up (SAI_ERR_TIMEOUT in *d_err), the rows of
  * dq and dw that were not formed are NaN, and all of dk.
- * dk of tokens split over calls (t_begin) is the sum of the calls' dk. Errors:
+ * dk of tokens split over calls (t_begin) is the sum of the calls' dk, each of
+ * which has been rounded to bf16. The workspace holds G also where idx is NULL,
+ * although dscores is read in its place. Errors:
  * as for sai_indexer_scores, and SAI_ERR_WORKSPACE.
  */
 size_t sai_indexer_scores_backward_workspace_bytes(int B, int S, int H, int D, int P);

@@ -18,10 +18,11 @@
 // Bound: the epilogue. A 128 x 256 tile of D = 128 is 512 cycles of MMA, but its
 // 32,768 products each take an integer instruction (relu and conversion in one)
 // and half of a packed subtraction and of a packed fma: about 800 cycles with the
-// tensor-memory loads on the four schedulers (measured alone), 1,700 with a
-// tile's hand-overs. Taken from there: the column weights are held in registers
+// tensor-memory loads on the four schedulers (measured alone); 0.41 ms at S = 16384
+// are about 1,800 cycles a tile, the rest of which is the chain of a tile's loads,
+// barriers and hand-overs. Taken from there: the column weights are held in registers
 // over an item's tiles (as broadcasts from shared memory they fill 1,024 cycles a
-// tile with register bytes: 0.56 ms against 0.46 at S = 16384), and a tile's two
+// tile with register bytes: 0.56 ms against 0.46 when that was tried), and a tile's two
 // barriers are tested together. At few tokens a sequence a tile has few columns, and
 // the producers' instructions and the keys' arrival bind.
 //
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
     // One item of every gridDim.x. Whole token tiles come longest first and are taken
     // there and back: the CTA with the longest of one round takes the shortest of the
     // next (always from the same end, the first CTA had 35 key tiles at S = 4096 where
-    // the mean is 31: 42.4 us against 40.8). Split ones have no such order (a decoding
-    // batch takes 42.2 us as it is, 43.6 there and back).
+    // the mean is 31: 40.9 us against 39.0). Split ones have no such order (a decoding
+    // batch takes 36.1 us as it is, 37.2 there and back).
     const int rounds = p.n_items / (int)gridDim.x, back = p.chunk == p.n_kt;
     auto item_of = [&](int n) {
         return n * (int)gridDim.x + ((n & back) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -651,7 +652,7 @@ cudaError_t launch_indexer_scores(const ScoresArgs &a, cudaStream_t stream)
     p.n_kt = (a.P + 127) / 128;
     // Few token tiles (decoding): the keys are split too, into about eight items
     // an SM, but an item has four key tiles where that leaves two an SM (at one tile an
-    // item the items' preparation bound: 32 x 2 tokens over 8192 entries took 23 us, 16
+    // item the items' preparation bound: 32 x 2 tokens over 8192 entries take 20.8 us, 14.7
     // with four). With four token tiles an SM or more their unequal lengths even out
     // over the CTAs, and an item's query tile is best read once.
     const long long rows = (long long)a.B * p.n_tt;
@@ -665,9 +666,9 @@ cudaError_t launch_indexer_scores(const ScoresArgs &a, cudaStream_t stream)
         return cudaErrorInvalidValue;
     p.n_items = (int)items;
     // Split items have few columns a tile, so that one producer's 1,150 cycles a tile
-    // bound them (32 x 2 tokens over 16 to 33 thousand entries: 42.5 us, 38.5 with two);
+    // bound them (32 x 2 tokens over 16 to 33 thousand entries: 44.5 us, 36.1 with two);
     // whole ones are better served by two warps that prepare items (a packed batch:
-    // 25.9 us, 30.4 with one).
+    // 26.4 us, 31.2 with one).
     p.producers = p.chunk < p.n_kt && p.chunk >= 2 ? 2 : 1;
     p.box_rows = a.map.page < 128 ? a.map.page : 128;
     p.loads = a.map.max_pages > 1 && a.map.page < 128 ? 128 / a.map.page : 1;

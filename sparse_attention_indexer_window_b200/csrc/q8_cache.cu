@@ -7,7 +7,8 @@
 //     int8:  code = rint(127 x / amax),  scale = amax / 127
 //     e4m3:  code = e4m3(448 x / amax),  scale = amax / 448
 //   (ties to even; amax = 0: codes 0, scale 0; a NaN or infinity in the group:
-//   codes 0, scale NaN), and is read back as code * scale.
+//   codes 0, scale NaN), and is read back as code * scale, formed in fp32 and then
+//   rounded to the rows' type.
 //
 // The codes are those of the formula in exact arithmetic. For 16-bit inputs
 // one correctly rounded quotient is enough: lim * x is exact in fp32, and a
