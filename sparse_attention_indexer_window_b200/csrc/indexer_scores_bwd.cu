@@ -35,9 +35,14 @@
 // each key: with one for the batch, a token's dq and a key's dk were lost where their
 // gradients were 2^-35 of others'.
 //
-// Bound: per 128 x 128 tile of D = 128, 256 cycles of kind::i8 and 512 of
-// kind::f16 on the tensor pipe. The two stationary tiles alternate: while one's
-// M is formed the other's products run. Warp roles: warp 0 TMA, warps 1 and 2
+// Bound: the chain of products, M and products through tensor memory. Per 128 x 128
+// tile of D = 128 the tensor pipe has 256 cycles of kind::i8 and 512 of kind::f16, and is
+// busy for a third of dq's time and two fifths of dk's. In dq an item's end adds to it,
+// where the accumulator is read before M is handed over: 82 us at S = 4096 are about 5,000
+// cycles a step of two tiles, 0.81 ms at S = 16384, whose items are longer, about 3,500.
+// The two stationary tiles alternate: while one's M is formed the other's products
+// run. Tiles are walked whatever is selected in them, up to the last that the tokens can
+// see: the cost does not fall with K or with documents that end earlier. Warp roles: warp 0 TMA, warps 1 and 2
 // issue the MMAs of one tile each (one warp for both left the tensor pipe idle
 // through its waits), warps 4..11 and 12..19 the epilogues of the two tiles (two
 // warps for each 32 lanes, 64 columns each). The halves are four chains of
@@ -336,7 +341,7 @@ __device__ __forceinline__ int share_start(const BwPlan &p, int x) { return x * 
 // late tokens, which have the most key tiles, first) of every gridDim.x, there and
 // back: the CTA with the longest item of one round takes the shortest of the next
 // (always from the same end, the first CTA had 35 steps at S = 4096 where the mean
-// is 31, and the whole call took 173 us against 169). dk walks a contiguous share
+// is 31, and the whole call takes 178 us against 176). dk walks a contiguous share
 // of all steps of the batch (a pair of key tiles times the token tiles that see
 // it), so its share may end inside a pair.
 template <int MODE>

@@ -20,8 +20,10 @@
 // rounded. Three instructions a value; a full division for each value bound
 // the kernel (52 us for 8 x 8192 rows of 512 against 15 us of HBM time).
 //
-// Bound: HBM (each value is read and each code written once); at a few rows,
-// the launch. One group is held by group/8 lanes, 8 values (one or two 16-byte
+// Bound: each value is read and each code written once (15 us of HBM for 8 x 8192
+// rows of 512); the write takes 31 us of it, bound by its instructions (issue 0.75 a
+// scheduler: about 25 a value), the read 20, bound by its loads' latency; a few
+// rows the launch. One group is held by group/8 lanes, 8 values (one or two 16-byte
 // loads) each, its maximum found by shuffles, so that a row is read once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
