@@ -655,8 +655,8 @@ sai_status sai_indexer_scores(const int8_t *q8, const float *q_scale, const floa
  *   workspace device scratch of sai_indexer_scores_backward_workspace_bytes()
  *            bytes, 16-byte aligned; its content need not be kept
  *
- * Where a wait inside a kernel gave up (SAI_ERR_TIMEOUT in *d_err), the rows of
- * dq and dw that were not formed are NaN, and all of dk.
+ * Where a wait inside a kernel gave up (SAI_ERR_TIMEOUT in *d_err), dq, dk and dw
+ * are NaN.
  * dk of tokens split over calls (t_begin) is the sum of the calls' dk, each of
  * which has been rounded to bf16. The workspace holds G also where idx is NULL,
  * although dscores is read in its place. Errors:

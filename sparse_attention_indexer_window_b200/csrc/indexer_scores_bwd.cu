@@ -38,8 +38,8 @@
 // Bound: the chain of products, M and products through tensor memory. Per 128 x 128
 // tile of D = 128 the tensor pipe has 256 cycles of kind::i8 and 512 of kind::f16, and is
 // busy for a third of dq's time and two fifths of dk's. In dq an item's end adds to it,
-// where the accumulator is read before M is handed over: 82 us at S = 4096 are about 5,000
-// cycles a step of two tiles, 0.81 ms at S = 16384, whose items are longer, about 3,500.
+// where the accumulator is read before M is handed over: 80 us at S = 4096 are about 4,900
+// cycles a step of two tiles, 0.80 ms at S = 16384, whose items are longer, about 3,450.
 // The two stationary tiles alternate: while one's M is formed the other's products
 // run. Tiles are walked whatever is selected in them, up to the last that the tokens can
 // see: the cost does not fall with K or with documents that end earlier. Warp roles: warp 0 TMA, warps 1 and 2
@@ -51,8 +51,7 @@
 // codes into scaled fp16; dq takes the keys in fp16 as bwd_prep_kernel wrote them
 // (turned into fp16 tile by tile they cost dq a sixth of its instructions), and
 // warps 20..23 stage gk. Every wait is bounded; on timeout the kernel records
-// SAI_ERR_TIMEOUT and unwinds: the rows of dq and dw that were not formed are NaN, and
-// all of dk.
+// SAI_ERR_TIMEOUT and unwinds, and bwd_reduce_kernel makes the call's outputs NaN.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -89,7 +88,7 @@ struct BwPlan {
     const float2 *row;     // [B,S] scale of the token's gk, the power of two above its |w qs|; 0, 0 where
                            // it has no gradient
     float *part;           // dk: [grid + B n_pairs][256][D]
-    uint32_t *gave_up;     // dk: not 0 where a wait gave up
+    uint32_t *gave_up;     // not 0 where a wait gave up
 };
 
 // The power of two that brings a largest magnitude (bits) below 2^top, at
@@ -923,15 +922,11 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                     mbar_arrive(&sm->acc_empty[i]);
                 return true;
             };
-            auto row_of = [&]() {
-                const int t = wk.a0 + i * TT + tt;
-                return t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
-            };
             bool go = wk.begin(a, p), ok = true;
             while (go) {
                 if (wk.first) {
                     const int t = wk.a0 + i * TT + tt;
-                    row = row_of();
+                    row = t < a.S && h < a.H ? (uint32_t)(((int64_t)wk.b * a.S + t) * a.H + h) : kNone;
                     const float f = row != kNone ? __ldg(&p.row[(int64_t)wk.b * a.S + t].x) : 0.f;
                     any = f != 0.f;
                     const float inv = any ? inverse_pow2(f) : 0.f;
@@ -1007,27 +1002,8 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
             }
             if (pending && ok)
                 ok = finish();
-            // A wait gave up: NaN for the rows of the finished item, the current one and those
-            // behind it.
-            auto spoil = [&](uint32_t to) {
-                if (to == kNone)
-                    return;
-                if (!half)
-                    a.dw[to] = __int_as_float(0x7fc00000);
-                for (int c = 0; c < D / 2; ++c)
-                    a.dq[(int64_t)to * D + half * (D / 2) + c] = 0x7fc0;
-            };
-            if (!ok) {
-                if (pending)
-                    spoil(old_row);
-                spoil(row);
-                while (go) {
-                    if (wk.first)
-                        spoil(row_of());
-                    wk.s = wk.s_end - 1;
-                    go = wk.next(a, p);
-                }
-            }
+            if (!ok && lane == 0)
+                *p.gave_up = 1u;
         } else {
             // this key's gradients of the tokens of the warp's columns, read a step
             // ahead; lane e holds token e's power of two for its weights and its candidates,
@@ -1146,7 +1122,7 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
                 }
             }
             if (!ok && lane == 0)
-                *p.gave_up = 1u;                // partial sums are missing: no key's dk is right
+                *p.gave_up = 1u;
         }
     }
 
@@ -1158,13 +1134,13 @@ __global__ void __launch_bounds__(bw_threads(MODE == 0), 1)
     }
 }
 
-// dk: the partial sums of a pair's segments, added in a fixed order (NaN where
-// one is missing). One block a
+// dk: the partial sums of a pair's segments, added in a fixed order. One block a
 // key; the segments are cut into 1024 / D runs of neighbours, whose sums are
 // added in order, so that the loads of a long list are in flight together.
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, const BwPlan p)
 {
     __shared__ float4 run[256];
+    const bool gave_up = __ldg(p.gave_up) != 0u;
     const int b = (int)(blockIdx.x / (unsigned)a.P), j = (int)(blockIdx.x - (unsigned)b * (unsigned)a.P);
     const int kp = j >> 8, pair = b * p.n_pairs + kp;
     const int per_row = a.D / 4, runs = 256 / per_row;
@@ -1193,6 +1169,15 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, 
             s.w += v.w;
         }
     }
+    // a wait gave up, so that rows and partial sums are missing: no output is given out
+    if (gave_up) {
+        const int64_t rows = (int64_t)a.B * a.S * a.H, step = (int64_t)gridDim.x * blockDim.x;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows; i += step) {
+            a.dw[i] = __int_as_float(0x7fc00000);
+            for (int c = 0; c < a.D / 8; ++c)
+                reinterpret_cast<uint4 *>(a.dq + i * a.D)[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        }
+    }
     run[threadIdx.x] = s;
     __syncthreads();
     if (me)
@@ -1204,7 +1189,7 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const ScoresBwdArgs a, 
         s.z += v.z;
         s.w += v.w;
     }
-    if (__ldg(p.gave_up) != 0u)
+    if (gave_up)
         s.x = s.y = s.z = s.w = __int_as_float(0x7fc00000);
     const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
     *reinterpret_cast<uint2 *>(a.dk + (int64_t)blockIdx.x * a.D + c) =
